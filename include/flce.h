@@ -77,8 +77,10 @@ extern "C" {
 /* Opaque CUDA stream (the runtime's cudaStream_t). */
 typedef struct CUstream_st* flce_stream_t;
 
-/* Element types of hidden, weight, bias and the gradients. */
-enum { FLCE_F32 = 0, FLCE_BF16 = 1 };
+/* Element types of hidden, weight, bias and the gradients.  FLCE_F16 is taken by
+ * the operators on either side of the head only (flce_add_rms_norm and below);
+ * the loss takes fp32 and bf16. */
+enum { FLCE_F32 = 0, FLCE_BF16 = 1, FLCE_F16 = 2 };
 
 /* Reduction of the per-token losses. */
 enum { FLCE_RED_NONE = 0, FLCE_RED_SUM = 1, FLCE_RED_MEAN = 2 };
@@ -349,6 +351,178 @@ FLCE_API int flce_forward_noalloc(const flce_problem* problem, const void* hidde
                                   const void* bias, const int64_t* targets, float* loss, float* lse,
                                   float* entropy, int64_t* correct, int64_t* n_valid, float* entropy_sum,
                                   flce_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Operators on either side of the head: the norm that produces `hidden`, the
+ * global norm and clipping of the gradients, and the penalties, biases and
+ * masks on logits.  The conventions above hold (caller-owned device memory of
+ * the current device, work enqueued on `stream`, status codes before anything
+ * is enqueued, fixed summation order, graph capture), except that
+ *   - matrices may have a stride between rows (elements; the elements of a row
+ *     are adjacent), and pointers need the alignment of their element type only
+ *     (FLCE_ERR_MISALIGNED otherwise); 16-byte aligned rows are faster;
+ *   - there is no device status word: nothing in the data is an error;
+ *   - their types are FLCE_F32, FLCE_BF16 and FLCE_F16.
+ * Sums, norms and softmax statistics are held in fp32 or fp64.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Root-mean-square norm of the rows of x, with an optional residual addition:
+ *   h    = rn(x + residual) in the residual's type (h = x without a residual)
+ *   rstd = 1 / sqrt(mean_j h_j^2 + eps)
+ *   y_j  = h_j * rstd * (weight_j + weight_offset)   (weight_j = 1 when NULL)
+ * y is a function of the stored (rounded) h, so that a backward that reads h
+ * differentiates what the forward computed.  The squares are summed in fp32.
+ *   rows          N >= 0
+ *   cols          1 <= D <= 131072
+ *   *_stride      elements between rows; outputs: >= cols when rows > 1; inputs:
+ *                 >= 0 (0 reads one row N times)
+ *   dtype         type of x, y (and dy, dx)
+ *   residual_dtype  type of residual, h, dh, dresidual: dtype or FLCE_F32; it
+ *                 must be dtype when there is no residual
+ *   weight_dtype  type of weight, dweight; ignored when weight is NULL
+ *   quant_group   8-bit output: columns per scale, 0 (one scale per row) or a
+ *                 multiple of 16; ignored by the other calls
+ *   eps           finite, >= 0
+ *   weight_offset finite: 0, or 1 for heads that store the weight minus one
+ */
+typedef struct {
+  int64_t rows, cols;
+  int64_t x_stride;         /* x, or dy in the backward                    */
+  int64_t residual_stride;  /* residual, or dh in the backward             */
+  int64_t h_stride;         /* h                                           */
+  int64_t y_stride;         /* y or q, or dx in the backward               */
+  int64_t dresidual_stride; /* dresidual; 0 outside the backward           */
+  int32_t dtype;
+  int32_t residual_dtype;
+  int32_t weight_dtype;
+  int32_t quant_group;
+  float eps;
+  float weight_offset;
+} flce_norm_problem;
+
+/*
+ * Forward.
+ *   x        [N, D]
+ *   residual [N, D] or NULL
+ *   weight   [D] or NULL
+ *   h        [N, D] written when there is a residual (may be the residual's own
+ *            memory), NULL without one
+ *   y        [N, D] (may be x's own memory)
+ *   rstd     [N] fp32 for the backward, or NULL
+ */
+FLCE_API int flce_add_rms_norm(const flce_norm_problem* problem, const void* x, const void* residual,
+                               const void* weight, void* h, void* y, float* rstd, flce_stream_t stream);
+
+/*
+ * Forward whose normalised output is held in 8 bits (e4m3, largest value 448):
+ * for each group of quant_group columns of a row (the last may be short)
+ *   scale = max_j |y_j| / 448,  q_j = e4m3(y_j / scale), 0 where scale is 0,
+ * with y in fp32.  A group with a NaN or an infinity gets a non-finite scale.
+ *   q      [N, D] bytes, y_stride between rows
+ *   scale  [N, ceil(D / group)] fp32, dense
+ */
+FLCE_API int flce_add_rms_norm_fp8(const flce_norm_problem* problem, const void* x, const void* residual,
+                                   const void* weight, void* h, void* q, float* scale, flce_stream_t stream);
+
+/* Bytes of device workspace flce_add_rms_norm_backward needs (needs no GPU). */
+FLCE_API int flce_add_rms_norm_workspace_size(const flce_norm_problem* problem, size_t* bytes);
+
+/*
+ * Backward: with g_j = dy_j (weight_j + weight_offset), n_j = h_j rstd and
+ * c = mean_j g_j n_j,
+ *   d_j       = rstd (g_j - n_j c) + dh_j   (dh_j = 0 when dh is NULL)
+ *   dx        = d in dtype, dresidual = d in residual_dtype (each may be NULL)
+ *   dweight_j = sum over rows of dy_j n_j, in weight_dtype (NULL: not formed)
+ *   dy  [N, D] gradient of y;  dh [N, D] gradient of h from its other uses
+ *   h, rstd: of the forward (h is x when there was no residual)
+ *   dx may be dy's own memory, and dresidual dh's.
+ */
+FLCE_API int flce_add_rms_norm_backward(const flce_norm_problem* problem, const void* dy, const void* h,
+                                        const void* weight, const float* rstd, const void* dh, void* dx,
+                                        void* dresidual, void* dweight, void* workspace, size_t workspace_bytes,
+                                        flce_stream_t stream);
+
+/* Bytes of device workspace the two calls below need for `count` tensors (needs no GPU). */
+FLCE_API int flce_grad_norm_workspace_size(int64_t count, size_t* bytes);
+
+/*
+ * The 2-norm of all elements of `count` dense tensors together:
+ *   *norm = sqrt(sum over tensors and elements of g^2)   fp32, on the device
+ * The squares are summed so that no finite gradient overflows or underflows
+ * (fp32 within small groups, fp64 across them and for extreme values).
+ *   grads   host array of device pointers (NULL allowed where numel is 0)
+ *   numel   host array of element counts, >= 0
+ *   dtypes  host array of FLCE_* types; they may differ
+ * The arrays are read before the call returns.
+ */
+FLCE_API int flce_grad_norm(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int64_t count,
+                            float* norm, void* workspace, size_t workspace_bytes, flce_stream_t stream);
+
+/*
+ * The same norm, and every gradient scaled so that it does not exceed max_norm:
+ *   c = min(1, max_norm / (*norm + 1e-6)),  out = rn(g * c)
+ * with an fp32 multiply and one rounding to the gradient's type.  A NaN norm
+ * gives NaN gradients; an infinite one c = 0.
+ *   outs    host array of device pointers: where each clipped gradient goes,
+ *           its own memory (in place) or a dense tensor of the same type that
+ *           overlaps no gradient.  In place, nothing is written when c is 1.
+ *   max_norm  >= 0, not NaN (infinity leaves the gradients as they are)
+ */
+FLCE_API int flce_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numel,
+                                 const int32_t* dtypes, int64_t count, float max_norm, float* norm, void* workspace,
+                                 size_t workspace_bytes, flce_stream_t stream);
+
+/*
+ * Logits of a batch of requests, made ready for choosing a token.
+ *   rows      B >= 0 requests
+ *   vocab     V, 1 <= V <= 2^30
+ *   history   H >= 0 columns of `tokens`;  n_bias  K >= 0 entries of a row's bias list
+ *   *_stride  elements between rows (mask: 32-bit words); inputs >= 0, out >= V
+ *             when rows > 1
+ *   logits_dtype, out_dtype: out_dtype is logits_dtype or FLCE_F32
+ *   tokens_i64, bias_ids_i64: 1 for int64 ids, 0 for int32 ids
+ */
+typedef struct {
+  int64_t rows, vocab, history, n_bias;
+  int64_t logits_stride, out_stride, tokens_stride, bias_ids_stride, bias_stride, mask_stride;
+  int32_t logits_dtype, out_dtype;
+  int32_t tokens_i64, bias_ids_i64;
+} flce_logits_problem;
+
+/* Bytes of device workspace flce_process_logits needs (needs no GPU). */
+FLCE_API int flce_process_logits_workspace_size(const flce_logits_problem* problem, size_t* bytes);
+
+/*
+ * For request b and vocabulary entry v, with z = logits[b, v] in fp32 and every
+ * step rounded to fp32:
+ *   1. v among tokens[b, :lens[b]]:  z = z > 0 ? z / repetition[b] : z * repetition[b]
+ *   2. n > 0 times v among tokens[b, prompt_lens[b]:lens[b]]:
+ *      z = z - frequency[b] * n, then z = z - presence[b]
+ *   3. v in bias_ids[b]:  z = z + (sum of its entries of bias[b], in order)
+ *   4. bit v % 32 of word v / 32 of mask[b] is 0:  z = -inf, whatever it was
+ *   out[b, v] = rn(z);  lse[b] = log sum_v exp(out[b, v])
+ *   token[b] = lowest v with the largest out[b, v]; -1 (and lse -inf) when every
+ *   entry is -inf.  A NaN that is not masked counts as the largest, and makes
+ *   lse NaN.
+ *   logits   [B, V]
+ *   tokens   [B, H] ids, or NULL (no history: steps 1 and 2 are left out, and the
+ *            five arguments after it must be NULL).  Ids outside [0, V) are padding.
+ *   lens, prompt_lens  [B] int64, clamped to [0, H]; NULL: H, and 0 (no prompt)
+ *   repetition, presence, frequency  [B] fp32, each NULL for none
+ *   bias_ids [B, K] ids and bias [B, K] fp32, both or neither; ids outside
+ *            [0, V) are padding
+ *   mask     [B, ceil(V / 32)] 32-bit words, or NULL
+ *   out      [B, V] (may be the logits' own memory when the types are the same)
+ *   token    [B] int64 or NULL;  lse [B] fp32 or NULL
+ */
+FLCE_API int flce_process_logits(const flce_logits_problem* problem, const void* logits, const void* tokens,
+                                 const int64_t* lens, const int64_t* prompt_lens, const float* repetition,
+                                 const float* presence, const float* frequency, const void* bias_ids,
+                                 const float* bias, const void* mask, void* out, int64_t* token, float* lse,
+                                 void* workspace, size_t workspace_bytes, flce_stream_t stream);
 
 /* Static English description of a status code (never NULL). */
 FLCE_API const char* flce_status_string(int status);

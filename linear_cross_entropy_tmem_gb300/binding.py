@@ -12,7 +12,7 @@ from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libflce.so")
 
-FLCE_F32, FLCE_BF16 = 0, 1
+FLCE_F32, FLCE_BF16, FLCE_F16 = 0, 1, 2
 FLCE_RED_NONE, FLCE_RED_SUM, FLCE_RED_MEAN = 0, 1, 2
 FLCE_FLAG_COMPACT_VALID = 1
 FLCE_FLAG_BWD_RECOMPUTE = 2
@@ -62,6 +62,45 @@ class FlceProblem(ctypes.Structure):
     ]
 
 
+class FlceNormProblem(ctypes.Structure):
+    """Mirror of ``flce_norm_problem``."""
+    _fields_ = [
+        ("rows", c_int64),
+        ("cols", c_int64),
+        ("x_stride", c_int64),
+        ("residual_stride", c_int64),
+        ("h_stride", c_int64),
+        ("y_stride", c_int64),
+        ("dresidual_stride", c_int64),
+        ("dtype", c_int32),
+        ("residual_dtype", c_int32),
+        ("weight_dtype", c_int32),
+        ("quant_group", c_int32),
+        ("eps", c_float),
+        ("weight_offset", c_float),
+    ]
+
+
+class FlceLogitsProblem(ctypes.Structure):
+    """Mirror of ``flce_logits_problem``."""
+    _fields_ = [
+        ("rows", c_int64),
+        ("vocab", c_int64),
+        ("history", c_int64),
+        ("n_bias", c_int64),
+        ("logits_stride", c_int64),
+        ("out_stride", c_int64),
+        ("tokens_stride", c_int64),
+        ("bias_ids_stride", c_int64),
+        ("bias_stride", c_int64),
+        ("mask_stride", c_int64),
+        ("logits_dtype", c_int32),
+        ("out_dtype", c_int32),
+        ("tokens_i64", c_int32),
+        ("bias_ids_i64", c_int32),
+    ]
+
+
 _LIB = None
 
 # name -> (restype, argtypes); every function ``include/*.h`` declares.
@@ -94,6 +133,16 @@ SIGNATURES = {
                                       c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "flce_forward_noalloc": (c_int, [POINTER(FlceProblem), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                      c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "flce_add_rms_norm": (c_int, [POINTER(FlceNormProblem)] + [c_void_p] * 7),
+    "flce_add_rms_norm_fp8": (c_int, [POINTER(FlceNormProblem)] + [c_void_p] * 7),
+    "flce_add_rms_norm_workspace_size": (c_int, [POINTER(FlceNormProblem), POINTER(c_size_t)]),
+    "flce_add_rms_norm_backward": (c_int, [POINTER(FlceNormProblem)] + [c_void_p] * 9 + [c_size_t, c_void_p]),
+    "flce_grad_norm_workspace_size": (c_int, [c_int64, POINTER(c_size_t)]),
+    "flce_grad_norm": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "flce_clip_grad_norm": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_float, c_void_p, c_void_p,
+                                    c_size_t, c_void_p]),
+    "flce_process_logits_workspace_size": (c_int, [POINTER(FlceLogitsProblem), POINTER(c_size_t)]),
+    "flce_process_logits": (c_int, [POINTER(FlceLogitsProblem)] + [c_void_p] * 14 + [c_size_t, c_void_p]),
     "flce_read_device_status": (c_int, [c_void_p, c_void_p, POINTER(c_int)]),
     "flce_status_string": (c_char_p, [c_int]),
     "flce_abi_version": (c_int, []),

@@ -1,6 +1,6 @@
 """In-tree build of ``libflce.so`` for sm_103a with nvcc (no cmake, no setuptools).
 
-The three translation units compile in parallel; the library is relinked only
+The translation units compile in parallel; the library is relinked only
 when a source or header is newer than it.  Output:
 ``linear_cross_entropy_tmem_gb300/_build/libflce.so``.
 
@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libflce.so")
-SOURCES = ["flce_api.cu", "flce_fwd.cu", "flce_bwd.cu", "flce_noalloc.cu"]
+SOURCES = ["flce_api.cu", "flce_fwd.cu", "flce_bwd.cu", "flce_noalloc.cu", "flce_norm.cu", "flce_clip.cu", "flce_logits.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

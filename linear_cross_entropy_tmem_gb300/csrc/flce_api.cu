@@ -14,14 +14,9 @@
 #include <vector>
 
 #include "flce.h"
+#include "flce_host.h"
 #include "flce_launch.h"
 #include "flce_testing.h"
-
-#define FLCE_TRY(expr)               \
-  do {                               \
-    const int rc_ = (expr);          \
-    if (rc_ != FLCE_OK) return rc_;  \
-  } while (0)
 
 namespace flce {
 namespace {
@@ -51,16 +46,11 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int max_splits(int64_t rows) { return rows <= kSmallBatchRows ? kMaxSplitsSmall : kMaxSplits; }
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-struct DeviceInfo {
-  bool init = false;
-  int index = 0;
-  int num_sms = 0;
-  int major = 0, minor = 0;
-};
-
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+}  // namespace
 
 int get_device(DeviceInfo* out) {
   int dev = -1;
@@ -88,6 +78,8 @@ int get_device(DeviceInfo* out) {
   if (d.major != 10 || d.minor != 3) return FLCE_ERR_UNSUPPORTED_DEVICE;
   return FLCE_OK;
 }
+
+namespace {
 
 // 2-D bf16 tensor map with 128-byte swizzle; out-of-range elements read as 0.
 int make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
@@ -118,6 +110,8 @@ int make_store_map(CUtensorMap* m, void* base, bool f32, uint64_t cols, uint64_t
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+}  // namespace
+
 // The operands the tensor maps and the products address (hidden, weight, the
 // gradients, the workspace) must be memory of the current device: device
 // memory of this GPU or managed memory.  Host memory (pageable, pinned or
@@ -134,11 +128,8 @@ int check_local(const DeviceInfo& dev, const void* p) {
   if (a.type == cudaMemoryTypeDevice && a.device == dev.index) return FLCE_OK;
   return FLCE_ERR_INVALID_ARG;
 }
-template <class... P>
-int check_local(const DeviceInfo& dev, const void* p, P... rest) {
-  FLCE_TRY(check_local(dev, p));
-  return check_local(dev, rest...);
-}
+
+namespace {
 
 int validate(const flce_problem* p) {
   if (!p) return FLCE_ERR_INVALID_ARG;
@@ -513,15 +504,15 @@ int32_t g_log_cap = 0;
 int32_t* g_log_count = nullptr;
 std::atomic<int64_t> g_launches{0};
 
-// Runs `launch` (returning cudaError_t) on `st`, bracketed by logged events
-// when the launch log is on; counts the launch.
-template <class F>
-int logged(int kind, cudaStream_t st, F&& launch) {
-  flce_launch_record* rec = nullptr;
-  if (g_log && g_log_count && *g_log_count < g_log_cap) rec = &g_log[*g_log_count];
-  if (rec && cudaEventRecord(static_cast<cudaEvent_t>(rec->begin_event), st) != cudaSuccess) return FLCE_ERR_CUDA;
-  const cudaError_t e = launch();
-  if (e != cudaSuccess) return FLCE_ERR_CUDA;
+}  // namespace
+
+int log_begin(cudaStream_t st, flce_launch_record** rec) {
+  *rec = nullptr;
+  if (g_log && g_log_count && *g_log_count < g_log_cap) *rec = &g_log[*g_log_count];
+  if (*rec && cudaEventRecord(static_cast<cudaEvent_t>((*rec)->begin_event), st) != cudaSuccess) return FLCE_ERR_CUDA;
+  return FLCE_OK;
+}
+int log_end(int kind, cudaStream_t st, flce_launch_record* rec) {
   g_launches.fetch_add(1);
   if (rec) {
     if (cudaEventRecord(static_cast<cudaEvent_t>(rec->end_event), st) != cudaSuccess) return FLCE_ERR_CUDA;
@@ -531,7 +522,6 @@ int logged(int kind, cudaStream_t st, F&& launch) {
   return FLCE_OK;
 }
 
-}  // namespace
 }  // namespace flce
 
 using namespace flce;

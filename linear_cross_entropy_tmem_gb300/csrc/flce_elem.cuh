@@ -1,0 +1,93 @@
+// flce_elem.cuh — element types, vectors and reductions of the operators on
+// either side of the head (norm, gradient clipping, logit processing).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "flce.h"
+
+namespace flce {
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+
+// V adjacent elements, loaded and stored as 16-byte words (V * sizeof(T) is 16,
+// 32, or one element's size for V = 1).
+template <class T, int V>
+struct alignas(V * sizeof(T) < 16 ? V * sizeof(T) : 16) Vec {
+  T v[V];
+};
+
+template <class T, int V>
+__device__ __forceinline__ Vec<T, V> load_vec(const T* p) { return *reinterpret_cast<const Vec<T, V>*>(p); }
+template <class T, int V>
+__device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& x) { *reinterpret_cast<Vec<T, V>*>(p) = x; }
+
+template <int V>
+__device__ __forceinline__ void load_as_f32(const void* p, int dtype, int64_t i, float (&out)[V]) {
+  if (dtype == FLCE_F32) {
+    const Vec<float, V> x = load_vec<float, V>(static_cast<const float*>(p) + i);
+#pragma unroll
+    for (int k = 0; k < V; ++k) out[k] = x.v[k];
+  } else if (dtype == FLCE_BF16) {
+    const Vec<__nv_bfloat16, V> x = load_vec<__nv_bfloat16, V>(static_cast<const __nv_bfloat16*>(p) + i);
+#pragma unroll
+    for (int k = 0; k < V; ++k) out[k] = to_f32(x.v[k]);
+  } else {
+    const Vec<__half, V> x = load_vec<__half, V>(static_cast<const __half*>(p) + i);
+#pragma unroll
+    for (int k = 0; k < V; ++k) out[k] = to_f32(x.v[k]);
+  }
+}
+
+__device__ __forceinline__ void store_as(void* p, int dtype, int64_t i, float x) {
+  if (dtype == FLCE_F32) {
+    static_cast<float*>(p)[i] = x;
+  } else if (dtype == FLCE_BF16) {
+    static_cast<__nv_bfloat16*>(p)[i] = from_f32<__nv_bfloat16>(x);
+  } else {
+    static_cast<__half*>(p)[i] = from_f32<__half>(x);
+  }
+}
+
+// Sums over a warp (every lane gets the same value, in a fixed order).
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Sum over the block (every thread gets it); `buf` holds 32 values, and the
+// call after next may reuse it (callers in a loop alternate two buffers).
+template <class F>
+__device__ __forceinline__ F block_sum(F x, F* buf) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = (blockDim.x + 31) >> 5;
+  x = warp_sum(x);
+  if (lane == 0) buf[warp] = x;
+  __syncthreads();
+  return warp_sum(lane < warps ? buf[lane] : F(0));
+}
+
+inline size_t elem_size(int32_t dtype) { return dtype == FLCE_F32 ? 4 : 2; }
+inline bool known_dtype(int32_t dtype) { return dtype == FLCE_F32 || dtype == FLCE_BF16 || dtype == FLCE_F16; }
+inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+}  // namespace flce
