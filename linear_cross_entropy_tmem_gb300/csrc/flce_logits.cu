@@ -7,9 +7,14 @@
 //   token = lowest argmax out,  lse = log sum exp out
 //
 // The bound is memory: logits read once, out written once.  A block takes a
-// tile of one row's vocabulary; it counts the row's history into a table of the
-// tile in shared memory (integer atomics: the order does not matter), so that
-// the penalties are applied while the tile streams through registers.
+// tile of one row's vocabulary and holds it in registers: its loads are issued
+// first, and while they are under way the block works on the few entries that
+// the row's history and biases name.  It counts the history into a table of the
+// tile in shared memory (integer atomics: their order does not matter), then
+// one thread per named entry works out its new value, leaves it in the table
+// and marks it in a bitmap.  The dense pass only looks at the bitmap: a test per
+// vector instead of a table look-up and a division's code per entry.  Rounding,
+// maximum and sum come from registers, the maximum before the first exponential.
 #include <algorithm>
 #include <cmath>
 
@@ -21,10 +26,15 @@ namespace flce {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int64_t kMinTile = 1024;
-constexpr int64_t kMaxTile = 16384;     // 64 KB of counts (and 64 KB of biases)
-constexpr int64_t kWantBlocks = 608;    // four blocks on each of 152 SMs
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kMaxPerThread = 32;       // entries a thread holds, at most: a tile of 8192
+constexpr int kMaxSingles = 16;         // the same without vectors (a mask word per entry takes registers)
+constexpr int64_t kWantBlocks = 456;    // three blocks on each of 152 SMs
+// A word of the table: how often an entry was answered, and whether the prompt
+// has it; later the entry's new value.
 constexpr uint32_t kPromptBit = 0x80000000u;
+constexpr uint32_t kCountMask = kPromptBit - 1;
+constexpr uint32_t kFull = 0xffffffffu;
 
 struct Partial {
   float m;       // largest out of the tile (NaN above all)
@@ -46,12 +56,10 @@ struct LogitsParams {
   int64_t ls, os, ts, bis, bs, ms;
   int64_t history;
   int32_t n_bias;
-  int32_t vocab, tile, tiles;
+  int32_t vocab, tiles;
   int32_t tokens_i64, bias_ids_i64;
 };
 
-// Running softmax statistics of one thread: indexes come in ascending order, so
-// a strict comparison keeps the lowest.
 struct Stat {
   float m = -INFINITY, s = 0.f;
   int idx = INT32_MAX;
@@ -66,7 +74,8 @@ __device__ __forceinline__ bool before(float bm, int bi, float am, int ai) {
   return bi < ai;
 }
 
-// e^(m - top) of a part of a sum, with nothing for an empty part.
+// e^(m - top) of a part of a sum, with nothing for an empty part.  (The
+// difference first: m * log2(e) overflows for values near the type's lowest.)
 __device__ __forceinline__ float rescale(float m, float top) {
   return m == -INFINITY ? 0.f : ex2_approx((m - top) * kLog2e);
 }
@@ -81,9 +90,9 @@ __device__ __forceinline__ void warp_merge(Stat& a) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     Stat b;
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-    b.idx = __shfl_xor_sync(0xffffffffu, a.idx, o);
+    b.m = __shfl_xor_sync(kFull, a.m, o);
+    b.s = __shfl_xor_sync(kFull, a.s, o);
+    b.idx = __shfl_xor_sync(kFull, a.idx, o);
     // both sides of a pair add in the same order
     if ((threadIdx.x & o) == 0) {
       merge(a, b);
@@ -94,149 +103,326 @@ __device__ __forceinline__ void warp_merge(Stat& a) {
   }
 }
 
-__device__ __forceinline__ int64_t load_id(const void* p, int i64, int64_t i) {
-  return i64 ? static_cast<const int64_t*>(p)[i] : int64_t(static_cast<const int32_t*>(p)[i]);
+// The largest of three values, a NaN if any is one.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Largest value over the warp (NaN above all), by the order of its bits as a
+// signed integer; -0 counts as +0.
+__device__ __forceinline__ float warp_max(float x) {
+  const int bits = x != x ? 0x7fffffff : __float_as_int(x + 0.f);
+  const int key = bits >= 0 ? bits : bits ^ 0x7fffffff;
+  const int top = __reduce_max_sync(kFull, key);
+  return __int_as_float(top >= 0 ? top : top ^ 0x7fffffff);
 }
 
-// Counts the row's history into the tile's table.
-__device__ __forceinline__ void count_history(const LogitsParams& p, int64_t row, int v0, int n, uint32_t* counts) {
-  const int64_t len = p.lens ? min(max(p.lens[row], int64_t(0)), p.history) : p.history;
-  const int64_t prompt = p.prompt_lens ? min(max(p.prompt_lens[row], int64_t(0)), p.history) : 0;
-  for (int64_t i = threadIdx.x; i < len; i += kRowThreads) {
-    const int64_t at = load_id(p.tokens, p.tokens_i64, row * p.ts + i) - v0;
-    if (at >= 0 && at < n) {
-      if (i < prompt) {
-        atomicOr(&counts[at], kPromptBit);
-      } else {
-        atomicAdd(&counts[at], 1u);
-      }
+// The entries of a tile: places [0, tile) stand for [first, first + tile), of
+// which `count` from `begin` on are in the row.
+struct Span {
+  int first, begin, count;
+};
+// An id's place in the tile, or -1 (padding among them).
+__device__ __forceinline__ int place(const Span& s, int64_t id) {
+  const int lo = int(id);
+  return (id >> 32) == 0 && unsigned(lo - s.begin) < unsigned(s.count) ? lo - s.first : -1;
+}
+__device__ __forceinline__ int place(const Span& s, int32_t id) {
+  return unsigned(id - s.begin) < unsigned(s.count) ? id - s.first : -1;
+}
+
+// A list of ids read by the block, kIds of them per thread under way at once.
+constexpr int kIds = 8;
+constexpr int kIdsBlock = kIds * kRowThreads;
+struct Ids {
+  const void* p;
+  int i64;
+  __device__ __forceinline__ void load(int base, int n, const Span& s, int (&at)[kIds]) const {
+    if (i64) {
+      load(static_cast<const int64_t*>(p), base, n, s, at);
+    } else {
+      load(static_cast<const int32_t*>(p), base, n, s, at);
     }
   }
-}
-
-// Adds the row's biases to the tile's table, entry by entry in order: one warp,
-// 32 entries at a time; of the lanes with the same id, the lowest adds all.
-__device__ __forceinline__ void add_biases(const LogitsParams& p, int64_t row, int v0, int n, float* biases) {
-  const int lane = threadIdx.x & 31;
-  for (int base = 0; base < p.n_bias; base += 32) {
-    const int i = base + lane;
-    int at = -1;
-    float b = 0.f;
-    if (i < p.n_bias) {
-      const int64_t a = load_id(p.bias_ids, p.bias_ids_i64, row * p.bis + i) - v0;
-      if (a >= 0 && a < n) {
-        at = int(a);
-        b = p.bias[row * p.bs + i];
-      }
+  template <class Id>
+  __device__ __forceinline__ void load(const Id* ids, int base, int n, const Span& s, int (&at)[kIds]) const {
+    Id id[kIds];
+#pragma unroll
+    for (int u = 0; u < kIds; ++u) {
+      const int i = base + u * kRowThreads + int(threadIdx.x);
+      id[u] = i < n ? ids[i] : Id(-1);
     }
-    const uint32_t same = __match_any_sync(0xffffffffu, at);
-    const bool lead = at >= 0 && lane == __ffs(same) - 1;
-    float sum = lead ? biases[at] : 0.f;
-    uint32_t todo = same;
-    while (__any_sync(0xffffffffu, lead && todo != 0)) {
-      const int src = todo ? __ffs(todo) - 1 : lane;
-      const float x = __shfl_sync(0xffffffffu, b, src);
-      if (lead && todo) sum += x;
-      todo &= todo - 1;
-    }
-    if (lead) biases[at] = sum;
-    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < kIds; ++u) at[u] = place(s, id[u]);
   }
-}
+  __device__ __forceinline__ int one(int i, const Span& s) const {
+    return i64 ? place(s, static_cast<const int64_t*>(p)[i]) : place(s, static_cast<const int32_t*>(p)[i]);
+  }
+};
 
-// One step of the chain for an entry of the history.
+// Steps 1 and 2 of the chain for an entry of the history.
 __device__ __forceinline__ float penalise(float z, uint32_t word, float rep, float pres, float freq, bool has_rep) {
   if (has_rep) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-  const uint32_t n = word & ~kPromptBit;
+  const uint32_t n = word & kCountMask;
   if (n) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, float(n))), pres);
   return z;
 }
 
-template <class T, class O, int V>
-__global__ void __launch_bounds__(kRowThreads) process_logits_kernel(LogitsParams p) {
-  extern __shared__ __align__(16) uint32_t table[];
-  __shared__ Stat red[kRowThreads / 32];
+// A tile's marks: bit i of the bitmap for place i.
+__device__ __forceinline__ bool marked(const uint32_t* map, int at) { return (map[at >> 5] >> (at & 31)) & 1u; }
+// Marks a place; true for the one call that does.
+__device__ __forceinline__ bool mark(uint32_t* map, int at) {
+  const uint32_t bit = 1u << (at & 31);
+  return !(atomicOr(&map[at >> 5], bit) & bit);
+}
+
+// What the row's history and biases say of a tile, in shared memory.
+template <int kTile>
+struct Named {
+  uint32_t table[kTile];      // counts, then new values at the marked places
+  uint32_t map[kTile / 32];   // marks
+  uint32_t seen[kTile / 32];  // places that a bias names
+  int n_list;                 // entries of the list
+  int biased, twice;          // whether a bias names a place, or one twice
+  int pad;
+  uint16_t list[kTile];       // the places that the history names, each once
+};
+
+// Whoever meets a place first puts it on the list; whole warps.
+template <int kTile>
+__device__ __forceinline__ void append(Named<kTile>& s, int at, bool fresh) {
+  const uint32_t who = __ballot_sync(kFull, fresh);
+  if (!who) return;
+  const int lane = threadIdx.x & 31;
+  int pos = 0;
+  if (lane == 0) pos = atomicAdd(&s.n_list, __popc(who));
+  pos = __shfl_sync(kFull, pos, 0) + __popc(who & ((1u << lane) - 1));
+  if (fresh) s.list[pos] = uint16_t(at);
+}
+
+// A block's tile is kRowThreads * V * NV entries; thread t holds the vectors at
+// (t + i * kRowThreads) * V.  Vectors are aligned in memory: a row whose first
+// element is `shift` elements past a 16-byte boundary starts `shift` entries
+// into its first vector (V = 1: no shift).
+template <class T, class O, int V, int NV>
+__global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logits_kernel(LogitsParams p) {
+  constexpr int kTile = kRowThreads * V * NV;
+  extern __shared__ __align__(16) uint32_t smem[];
+  Named<kTile>& s = *reinterpret_cast<Named<kTile>*>(smem);
+  __shared__ Stat red[kRowWarps];
   const int64_t row = blockIdx.x / p.tiles;
   const int tile = int(blockIdx.x % p.tiles);
-  const int v0 = tile * p.tile;
-  const int n = min(p.tile, p.vocab - v0);
-  uint32_t* counts = table;
-  float* biases = reinterpret_cast<float*>(table + (p.tokens ? p.tile : 0));
-  if (p.tokens || p.n_bias) {
-    const int words = (p.tokens ? p.tile : 0) + (p.n_bias ? p.tile : 0);
-    for (int i = threadIdx.x * 4; i < words; i += kRowThreads * 4) *reinterpret_cast<uint4*>(table + i) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    if (p.n_bias && threadIdx.x < 32) add_biases(p, row, v0, n, biases);
-    if (p.tokens) count_history(p, row, v0, n, counts);
-    __syncthreads();
+  const T* logits = static_cast<const T*>(p.logits) + row * p.ls;
+  O* out = static_cast<O*>(p.out) + row * p.os;
+  const int shift = V == 1 ? 0 : int((reinterpret_cast<uintptr_t>(logits) / sizeof(T)) % V);
+  Span span;
+  span.first = tile * kTile - shift;  // < 0 in a shifted first tile
+  span.begin = max(span.first, 0);
+  span.count = min(span.first + kTile, p.vocab) - span.begin;
+  const int first = span.first;
+
+  // The loads of the lists and of the tile go out together.  The first ids are
+  // loaded whatever the row's length, which is under way too.
+  const bool named = p.tokens || p.n_bias;
+  const int history = p.tokens ? int(p.history) : 0;
+  const Ids ids = {p.tokens_i64 ? static_cast<const void*>(static_cast<const int64_t*>(p.tokens) + row * p.ts)
+                                : static_cast<const void*>(static_cast<const int32_t*>(p.tokens) + row * p.ts),
+                   p.tokens_i64};
+  const Ids bias_ids = {p.bias_ids_i64
+                            ? static_cast<const void*>(static_cast<const int64_t*>(p.bias_ids) + row * p.bis)
+                            : static_cast<const void*>(static_cast<const int32_t*>(p.bias_ids) + row * p.bis),
+                        p.bias_ids_i64};
+  int ids_at[kIds];
+  int bias_at = -1;
+  float f[NV][V];
+  uint32_t bits[NV];
+  if (history) ids.load(0, history, span, ids_at);
+  if (int(threadIdx.x) < p.n_bias) bias_at = bias_ids.one(threadIdx.x, span);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = first + (int(threadIdx.x) + i * kRowThreads) * V;
+    if (v >= 0 && v + V <= p.vocab) {
+      const Vec<T, V> x = load_vec<T, V>(logits + v);
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[i][k] = to_f32(x.v[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[i][k] = v + k >= 0 && v + k < p.vocab ? to_f32(logits[v + k]) : -INFINITY;
+    }
+    bits[i] = kFull;
+    if (p.mask && v > -V && v < p.vocab) {
+      const uint32_t* m = p.mask + row * p.ms;
+      if (shift == 0) {  // V divides 32: a vector's bits are in one word
+        bits[i] = m[v >> 5] >> (v & 31);
+      } else if (v >= 0) {
+        const int last = min(v + V, p.vocab) - 1;
+        bits[i] = m[v >> 5] >> (v & 31);
+        if ((last >> 5) != (v >> 5)) bits[i] |= m[last >> 5] << (32 - (v & 31));
+      } else {
+        bits[i] = m[0] << -v;
+      }
+    }
   }
-  const bool has_rep = p.repetition != nullptr;
-  const float rep = has_rep ? p.repetition[row] : 1.f;
-  const float pres = p.presence ? p.presence[row] : 0.f;
-  const float freq = p.frequency ? p.frequency[row] : 0.f;
-  const T* logits = static_cast<const T*>(p.logits) + row * p.ls + v0;
-  O* out = static_cast<O*>(p.out) + row * p.os + v0;
-  const uint32_t* mask = p.mask ? p.mask + row * p.ms + v0 / 32 : nullptr;
-  Stat st;
-  for (int i = threadIdx.x * V; i < n; i += kRowThreads * V) {
-    const Vec<T, V> x = load_vec<T, V>(logits + i);
-    // V divides 32 and the tile is a multiple of 32: a vector's bits are in one word
-    const uint32_t bits = mask ? mask[i / 32] >> (i % 32) : 0xffffffffu;
+
+  if (named) {
+    constexpr int kWords = kTile + 2 * (kTile / 32) + 4;  // up to the list
+    for (int i = threadIdx.x * 4; i < kWords; i += kRowThreads * 4)
+      *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
+    const int len = p.lens ? int(min(max(p.lens[row], int64_t(0)), int64_t(history))) : history;
+    const int prompt = p.prompt_lens ? int(min(max(p.prompt_lens[row], int64_t(0)), int64_t(history))) : 0;
+    const bool has_rep = p.repetition != nullptr;
+    const float rep = has_rep ? p.repetition[row] : 1.f;
+    const float pres = p.presence ? p.presence[row] : 0.f;
+    const float freq = p.frequency ? p.frequency[row] : 0.f;
+    __syncthreads();
+
+    // Count the history; mark what the biases name.
+    for (int base = 0; base < len; base += kIdsBlock) {
+      if (base) ids.load(base, len, span, ids_at);
+#pragma unroll
+      for (int u = 0; u < kIds; ++u) {
+        const int warp0 = base + u * kRowThreads + int(threadIdx.x & ~31u);
+        if (warp0 >= len) break;
+        const int i = warp0 + int(threadIdx.x & 31);
+        const int at = i < len ? ids_at[u] : -1;
+        bool fresh = false;
+        if (at >= 0) {
+          const uint32_t old = i < prompt ? atomicOr(&s.table[at], kPromptBit) : atomicAdd(&s.table[at], 1u);
+          fresh = old == 0;
+        }
+        append(s, at, fresh);
+      }
+    }
+    for (int i = threadIdx.x; i < p.n_bias; i += kRowThreads) {
+      const int at = i < kRowThreads ? bias_at : bias_ids.one(i, span);
+      if (at >= 0) {
+        s.biased = 1;
+        if (!mark(s.seen, at)) s.twice = 1;
+      }
+    }
+    __syncthreads();
+
+    // One thread per listed place works out its value from the logit (in L1:
+    // the tile's loads have just passed there).
+    const int n = s.n_list;
+    for (int i = threadIdx.x; i < n; i += kRowThreads) {
+      const int at = s.list[i];
+      s.table[at] = __float_as_uint(penalise(to_f32(logits[first + at]), s.table[at], rep, pres, freq, has_rep));
+      mark(s.map, at);
+    }
+    __syncthreads();
+    if (s.biased) {
+      const float* bias = p.bias + row * p.bs;
+      auto add = [&](int at, float b) {
+        const float z = marked(s.map, at) ? __uint_as_float(s.table[at]) : to_f32(logits[first + at]);
+        s.table[at] = __float_as_uint(__fadd_rn(z, b));
+        mark(s.map, at);
+      };
+      if (!s.twice) {
+        for (int i = threadIdx.x; i < p.n_bias; i += kRowThreads) {
+          const int at = i < kRowThreads ? bias_at : bias_ids.one(i, span);
+          if (at >= 0) add(at, bias[i]);
+        }
+      } else if (threadIdx.x == 0) {  // in the list's order
+        for (int i = 0; i < p.n_bias; ++i) {
+          const int at = bias_ids.one(i, span);
+          if (at >= 0) add(at, bias[i]);
+        }
+      }
+      __syncthreads();
+    }
+  }
+
+  // `at_top` is the lowest vector with the thread's maximum; which of its
+  // entries it is, the merge looks up in `out`.
+  float top = -INFINITY;
+  int at_top = INT32_MAX;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int at = (int(threadIdx.x) + i * kRowThreads) * V;
+    const int v = first + at;
+    if (named) {
+      const uint32_t w = s.map[at >> 5] >> (at & 31);
+      if (w & ((1u << V) - 1)) {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if ((w >> k) & 1u) f[i][k] = __uint_as_float(s.table[at + k]);
+      }
+    }
     Vec<O, V> o;
-    float f[V];
-    float top = -INFINITY;
-    bool nan = false;
+    float t = -INFINITY;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      float z = to_f32(x.v[k]);
-      if (p.tokens) {
-        const uint32_t word = counts[i + k];
-        if (word) z = penalise(z, word, rep, pres, freq, has_rep);
-      }
-      if (p.n_bias) {
-        const float b = biases[i + k];
-        if (b != 0.f) z = __fadd_rn(z, b);
-      }
-      if (!((bits >> k) & 1u)) z = -INFINITY;
-      o.v[k] = from_f32<O>(z);
-      f[k] = to_f32(o.v[k]);
-      nan |= f[k] != f[k];
-      top = fmaxf(top, f[k]);
+      if (!((bits[i] >> k) & 1u)) f[i][k] = -INFINITY;
+      o.v[k] = from_f32<O>(f[i][k]);
+      f[i][k] = to_f32(o.v[k]);
     }
-    store_vec<O, V>(out + i, o);
-    if (nan || top > st.m) {  // rare once a large value has been met
-      const float old = st.m;
+    // entries outside the row are -inf
+    if constexpr (V == 1) {
+      t = f[i][0];
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; k += 2) t = max3_nan(t, f[i][k], f[i][k + 1]);
+    }
+    if (t > top || (t != t && top == top)) {
+      top = t;
+      at_top = v;
+    }
+    if (v >= 0 && v + V <= p.vocab) {
+      store_vec<O, V>(out + v, o);
+    } else {
 #pragma unroll
       for (int k = 0; k < V; ++k)
-        if (before(f[k], v0 + i + k, st.m, st.idx)) {
-          st.m = f[k];
-          st.idx = v0 + i + k;
-        }
-      st.s *= rescale(old, st.m);
-    }
-    if (st.m != -INFINITY) {
-      // the difference first: m * log2(e) overflows for values near the type's lowest
-#pragma unroll
-      for (int k = 0; k < V; ++k) st.s += ex2_approx((f[k] - st.m) * kLog2e);
+        if (v + k >= 0 && v + k < p.vocab) out[v + k] = o.v[k];
     }
   }
-  warp_merge(st);
+
+  Stat st;
+  st.m = warp_max(top);
+  st.idx = __reduce_min_sync(kFull, top == st.m || (top != top && st.m != st.m) ? at_top : INT32_MAX);
+  if (st.m != -INFINITY) {
+    if constexpr (V == 1) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) sum += ex2_approx((f[i][0] - st.m) * kLog2e);
+      st.s = warp_sum(sum);
+    } else {  // two lanes of fp32 per instruction
+      const uint64_t neg = f2_splat(-st.m), l2e = f2_splat(kLog2e);
+      uint64_t sum = f2_splat(0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+          float a, b;
+          f2_unpack(f2_mul(f2_add(f2_pack(f[i][k], f[i][k + 1]), neg), l2e), a, b);
+          sum = f2_add(sum, f2_pack(ex2_approx(a), ex2_approx(b)));
+        }
+      float a, b;
+      f2_unpack(sum, a, b);
+      st.s = warp_sum(a + b);
+    }
+  }
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = st;
   __syncthreads();
   if (threadIdx.x < 32) {
-    if (threadIdx.x < kRowThreads / 32) st = red[threadIdx.x]; else st = Stat();
+    if (threadIdx.x < kRowWarps) st = red[threadIdx.x]; else st = Stat();
     warp_merge(st);
     if (threadIdx.x == 0) p.part[row * p.tiles + tile] = Partial{st.m, st.s, st.idx, 0};
   }
 }
 
-// One warp per row joins the tiles' statistics.
+// One warp per row joins the tiles' statistics, and finds the first entry of
+// the vector of `vec` that holds the maximum.
+template <class O>
 __global__ void __launch_bounds__(kRowThreads) merge_logits_kernel(const Partial* part, int64_t rows, int tiles,
-                                                               int64_t* token, float* lse) {
-  const int64_t row = blockIdx.x * int64_t(kRowThreads / 32) + (threadIdx.x >> 5);
+                                                                  const O* out, int64_t os, int vocab, int vec,
+                                                                  int64_t* token, float* lse) {
+  const int64_t row = blockIdx.x * int64_t(kRowWarps) + (threadIdx.x >> 5);
   if (row >= rows) return;
+  const int lane = threadIdx.x & 31;
   Stat st;
-  for (int i = threadIdx.x & 31; i < tiles; i += 32) {
+  for (int i = lane; i < tiles; i += 32) {
     const Partial q = part[row * tiles + i];
     Stat b;
     b.m = q.m;
@@ -245,12 +431,19 @@ __global__ void __launch_bounds__(kRowThreads) merge_logits_kernel(const Partial
     merge(st, b);
   }
   warp_merge(st);
-  if ((threadIdx.x & 31) == 0) {
-    const bool none = st.m == -INFINITY;
-    if (token) token[row] = none ? -1 : int64_t(st.idx);
-    // an infinite or NaN maximum is the sum
-    if (lse) lse[row] = none || st.m == INFINITY || st.m != st.m ? st.m : st.m + logf(st.s);
+  const bool none = st.m == -INFINITY;
+  if (token) {
+    bool hit = false;
+    const int v = st.idx + lane;
+    if (!none && lane < vec && v >= 0 && v < vocab) {
+      const float x = to_f32(out[row * os + v]);
+      hit = x == st.m || (x != x && st.m != st.m);
+    }
+    const uint32_t hits = __ballot_sync(kFull, hit);
+    if (lane == 0) token[row] = hits ? int64_t(st.idx + __ffs(hits) - 1) : -1;
   }
+  // an infinite or NaN maximum is the sum
+  if (lse && lane == 0) lse[row] = none || st.m == INFINITY || st.m != st.m ? st.m : st.m + logf(st.s);
 }
 
 // ---------------------------------------------------------------------------
@@ -258,19 +451,24 @@ __global__ void __launch_bounds__(kRowThreads) merge_logits_kernel(const Partial
 // ---------------------------------------------------------------------------
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tile width: enough blocks to fill the GPU, within what shared memory holds.
-int64_t plan_tile(int64_t rows, int64_t vocab) {
-  const int64_t per_row = std::max<int64_t>(1, cdiv(kWantBlocks, std::max<int64_t>(rows, 1)));
-  const int64_t tile = cdiv(cdiv(vocab, per_row), 128) * 128;
-  return std::min(std::max(tile, kMinTile), kMaxTile);
+// Entries per thread: as many as the registers hold, fewer where the blocks
+// would not fill the GPU.  (A tile of a row may start up to 7 places early.)
+int plan_per_thread(int64_t rows, int64_t vocab) {
+  int per = kMaxPerThread;
+  while (per > 4 && std::max<int64_t>(rows, 1) * cdiv(vocab + 7, kRowThreads * per) < kWantBlocks) per /= 2;
+  return per;
+}
+// Tiles of a row at most, whatever the form below.
+int64_t plan_tiles(int64_t rows, int64_t vocab) {
+  return cdiv(vocab + 7, int64_t(kRowThreads) * std::min(kMaxSingles, plan_per_thread(rows, vocab)));
 }
 
 int validate(const flce_logits_problem* p) {
   if (!p) return FLCE_ERR_INVALID_ARG;
   if (p->rows < 0 || p->vocab < 1 || p->vocab > (int64_t(1) << 30)) return FLCE_ERR_INVALID_ARG;
-  if (p->history < 0 || p->history > INT32_MAX || p->n_bias < 0 || p->n_bias > INT32_MAX - 32)
+  if (p->history < 0 || p->history > kCountMask || p->n_bias < 0 || p->n_bias > INT32_MAX - 32)
     return FLCE_ERR_INVALID_ARG;
-  if (p->rows > INT32_MAX / cdiv(p->vocab, plan_tile(p->rows, p->vocab))) return FLCE_ERR_INVALID_ARG;
+  if (p->rows > INT32_MAX / plan_tiles(p->rows, p->vocab)) return FLCE_ERR_INVALID_ARG;
   if (p->logits_stride < 0 || p->tokens_stride < 0 || p->bias_ids_stride < 0 || p->bias_stride < 0 ||
       p->mask_stride < 0 || (p->rows > 1 && p->out_stride < p->vocab) || p->out_stride < 0)
     return FLCE_ERR_INVALID_ARG;
@@ -279,21 +477,60 @@ int validate(const flce_logits_problem* p) {
   return FLCE_OK;
 }
 
-template <class T, class O, int V>
+// The kernel's form: vectors of `vec` entries, `nv` of them per thread.
+struct Form {
+  int vec, nv;
+  int32_t tiles;
+};
+// Vectors of 16 bytes where every row of logits and of out starts equally far
+// past a 16-byte boundary, in elements; else single elements.
+Form plan_form(const flce_logits_problem* p, const void* logits, const void* out) {
+  const int wide = int(16 / elem_size(p->logits_dtype));
+  const uint64_t a = reinterpret_cast<uintptr_t>(logits) / elem_size(p->logits_dtype);
+  const uint64_t b = reinterpret_cast<uintptr_t>(out) / elem_size(p->out_dtype);
+  const bool ok = (a - b) % wide == 0 && (p->rows == 1 || (p->logits_stride - p->out_stride) % wide == 0);
+  Form f;
+  f.vec = ok ? wide : 1;
+  const int per = plan_per_thread(p->rows, p->vocab);
+  f.nv = f.vec == 1 ? std::min(kMaxSingles, per) : std::max(1, per / f.vec);
+  f.tiles = int32_t(cdiv(p->vocab + f.vec - 1, int64_t(kRowThreads) * f.vec * f.nv));
+  return f;
+}
+
+template <class T, class O, int V, int NV>
 cudaError_t launch(const LogitsParams& p, int64_t rows, cudaStream_t st) {
-  const size_t smem = size_t(p.tile) * 4 * ((p.tokens ? 1 : 0) + (p.n_bias ? 1 : 0));
-  auto kern = process_logits_kernel<T, O, V>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxTile * 8));
+  auto kern = process_logits_kernel<T, O, V, NV>;
+  constexpr size_t kBytes = sizeof(Named<kRowThreads * V * NV>);
+  const size_t smem = p.tokens || p.n_bias ? kBytes : 0;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kBytes));
   if (e != cudaSuccess) return e;
   kern<<<unsigned(rows * p.tiles), kRowThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 template <class T, class O>
-cudaError_t launch_types(const LogitsParams& p, int64_t rows, bool vec, cudaStream_t st) {
-  // the last vector of a row must be whole
+cudaError_t launch_types(const LogitsParams& p, int64_t rows, const Form& f, cudaStream_t st) {
   constexpr int kV = 16 / sizeof(T);
-  if (vec && p.vocab % kV == 0) return launch<T, O, kV>(p, rows, st);
-  return launch<T, O, 1>(p, rows, st);
+  if (f.vec == kV) {
+    if (f.nv == 1) return launch<T, O, kV, 1>(p, rows, st);
+    if (f.nv == 2) return launch<T, O, kV, 2>(p, rows, st);
+    if (f.nv == 4) return launch<T, O, kV, 4>(p, rows, st);
+    if constexpr (kV == 4) {
+      if (f.nv == 8) return launch<T, O, kV, 8>(p, rows, st);
+    }
+  } else {
+    if (f.nv == 4) return launch<T, O, 1, 4>(p, rows, st);
+    if (f.nv == 8) return launch<T, O, 1, 8>(p, rows, st);
+    if (f.nv == 16) return launch<T, O, 1, 16>(p, rows, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <class O>
+cudaError_t launch_merge(const LogitsParams& q, int64_t rows, const Form& f, int64_t* token, float* lse,
+                         cudaStream_t st) {
+  merge_logits_kernel<O><<<unsigned(cdiv(rows, kRowWarps)), kRowThreads, 0, st>>>(
+      q.part, rows, q.tiles, static_cast<const O*>(q.out), q.os, q.vocab, f.vec, token, lse);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -306,8 +543,7 @@ extern "C" {
 int flce_process_logits_workspace_size(const flce_logits_problem* problem, size_t* bytes) {
   if (!bytes) return FLCE_ERR_INVALID_ARG;
   FLCE_TRY(validate(problem));
-  *bytes = size_t(problem->rows) * size_t(cdiv(problem->vocab, plan_tile(problem->rows, problem->vocab))) *
-               sizeof(Partial) + 256;
+  *bytes = size_t(problem->rows) * size_t(plan_tiles(problem->rows, problem->vocab)) * sizeof(Partial) + 256;
   return FLCE_OK;
 }
 
@@ -356,26 +592,24 @@ int flce_process_logits(const flce_logits_problem* problem, const void* logits, 
   q.history = p->history;
   q.n_bias = bias ? int32_t(p->n_bias) : 0;
   q.vocab = int32_t(p->vocab);
-  q.tile = int32_t(plan_tile(p->rows, p->vocab));
-  q.tiles = int32_t(cdiv(p->vocab, q.tile));
   q.tokens_i64 = p->tokens_i64;
   q.bias_ids_i64 = p->bias_ids_i64;
-  const bool vec = aligned_to(logits, 16) && aligned_to(out, 16) &&
-                   (p->rows == 1 || (p->logits_stride * el % 16 == 0 && p->out_stride * eo % 16 == 0));
+  const Form form = plan_form(p, logits, out);
+  q.tiles = form.tiles;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   FLCE_TRY(logged(FLCE_LAUNCH_OTHER, st, [&] {
-    if (p->logits_dtype == FLCE_F32) return launch_types<float, float>(q, p->rows, vec, st);
+    if (p->logits_dtype == FLCE_F32) return launch_types<float, float>(q, p->rows, form, st);
     if (p->logits_dtype == FLCE_BF16)
-      return p->out_dtype == FLCE_F32 ? launch_types<__nv_bfloat16, float>(q, p->rows, vec, st)
-                                      : launch_types<__nv_bfloat16, __nv_bfloat16>(q, p->rows, vec, st);
-    return p->out_dtype == FLCE_F32 ? launch_types<__half, float>(q, p->rows, vec, st)
-                                    : launch_types<__half, __half>(q, p->rows, vec, st);
+      return p->out_dtype == FLCE_F32 ? launch_types<__nv_bfloat16, float>(q, p->rows, form, st)
+                                      : launch_types<__nv_bfloat16, __nv_bfloat16>(q, p->rows, form, st);
+    return p->out_dtype == FLCE_F32 ? launch_types<__half, float>(q, p->rows, form, st)
+                                    : launch_types<__half, __half>(q, p->rows, form, st);
   }));
   if (!token && !lse) return FLCE_OK;
   return logged(FLCE_LAUNCH_OTHER, st, [&] {
-    merge_logits_kernel<<<unsigned(cdiv(p->rows, kRowThreads / 32)), kRowThreads, 0, st>>>(q.part, p->rows, q.tiles, token,
-                                                                                     lse);
-    return cudaGetLastError();
+    if (p->out_dtype == FLCE_F32) return launch_merge<float>(q, p->rows, form, token, lse, st);
+    if (p->out_dtype == FLCE_BF16) return launch_merge<__nv_bfloat16>(q, p->rows, form, token, lse, st);
+    return launch_merge<__half>(q, p->rows, form, token, lse, st);
   });
 }
 
