@@ -479,8 +479,8 @@ FLCE_API int flce_clip_grad_norm(const void* const* grads, void* const* outs, co
  * Logits of a batch of requests, made ready for choosing a token.
  *   rows      B >= 0 requests
  *   vocab     V, 1 <= V <= 2^30
- *   history   0 <= H < 2^30 columns of `tokens`;  n_bias  0 <= K < 2^31 - 32 entries
- *             of a row's bias list
+ *   history   0 <= H < 2^30 columns of `tokens`
+ *   n_bias    0 <= K < 2^30 entries of a row's bias list
  *   *_stride  elements between rows (mask: 32-bit words); inputs >= 0, out >= V
  *             when rows > 1
  *   logits_dtype, out_dtype: out_dtype is logits_dtype or FLCE_F32

@@ -35,6 +35,7 @@ constexpr int64_t kWantBlocks = 456;    // three blocks on each of 152 SMs
 constexpr uint32_t kPromptBit = 0x80000000u;
 constexpr uint32_t kCountMask = kPromptBit - 1;
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr int64_t kMaxIds = (int64_t(1) << 30) - 1;  // of a row's history, and of its biases
 
 struct Partial {
   float m;       // largest out of the tile (NaN above all)
@@ -161,6 +162,19 @@ struct Ids {
   }
 };
 
+// Sum of a row's biases of vocabulary entry v, in the list's order; whole warps.
+__device__ __forceinline__ float bias_sum(const Ids& ids, const float* bias, int n, int v) {
+  const Span one = {v, v, 1};
+  float sum = 0.f;
+  for (int base = 0; base < n; base += 32) {
+    const int i = base + int(threadIdx.x & 31);
+    const bool hit = i < n && ids.one(i, one) == 0;
+    const float b = hit ? bias[i] : 0.f;
+    for (uint32_t m = __ballot_sync(kFull, hit); m; m &= m - 1) sum = __fadd_rn(sum, __shfl_sync(kFull, b, __ffs(m) - 1));
+  }
+  return sum;
+}
+
 // Steps 1 and 2 of the chain for an entry of the history.
 __device__ __forceinline__ float penalise(float z, uint32_t word, float rep, float pres, float freq, bool has_rep) {
   if (has_rep) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
@@ -189,16 +203,45 @@ struct Named {
   uint16_t list[kTile];       // the places that the history names, each once
 };
 
-// Whoever meets a place first puts it on the list; whole warps.
+// Counts one id if `in`: the prompt's mark, or one more answer.  Returns the
+// word before (1 if not `in`).  Predicated rather than branched to, so that a
+// thread's kIds atomics are under way together.
+__device__ __forceinline__ uint32_t count_id(uint32_t* word, bool in, bool prompt) {
+  uint32_t old = 1u;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "setp.ne.u32 q, %3, 0;\n\t"
+      "@p atom.shared.or.b32 %0, [%1], %4;\n\t"
+      "@q atom.shared.add.u32 %0, [%1], 1;\n\t}\n"
+      : "+r"(old)
+      : "r"(smem_u32(word)), "r"(uint32_t(in && prompt)), "r"(uint32_t(in && !prompt)), "r"(kPromptBit)
+      : "memory");
+  return old;
+}
+
+// Whoever met a place first (the word before was 0) puts it on the list; whole
+// warps, one addition to the list's length for all of a warp's places.
 template <int kTile>
-__device__ __forceinline__ void append(Named<kTile>& s, int at, bool fresh) {
-  const uint32_t who = __ballot_sync(kFull, fresh);
-  if (!who) return;
+__device__ __forceinline__ void append(Named<kTile>& s, const int (&at)[kIds], const uint32_t (&old)[kIds]) {
   const int lane = threadIdx.x & 31;
+  int n = 0;
+#pragma unroll
+  for (int u = 0; u < kIds; ++u) n += old[u] == 0;
+  int before = n;  // places of the lanes up to this one
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int other = __shfl_up_sync(kFull, before, o);
+    if (lane >= o) before += other;
+  }
+  const int all = __shfl_sync(kFull, before, 31);
+  if (!all) return;
   int pos = 0;
-  if (lane == 0) pos = atomicAdd(&s.n_list, __popc(who));
-  pos = __shfl_sync(kFull, pos, 0) + __popc(who & ((1u << lane) - 1));
-  if (fresh) s.list[pos] = uint16_t(at);
+  if (lane == 31) pos = atomicAdd(&s.n_list, all);
+  pos = __shfl_sync(kFull, pos, 31) + before - n;
+#pragma unroll
+  for (int u = 0; u < kIds; ++u)
+    if (old[u] == 0) s.list[pos++] = uint16_t(at[u]);
 }
 
 // A block's tile is kRowThreads * V * NV entries; thread t holds the vectors at
@@ -211,8 +254,9 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
   extern __shared__ __align__(16) uint32_t smem[];
   Named<kTile>& s = *reinterpret_cast<Named<kTile>*>(smem);
   __shared__ Stat red[kRowWarps];
-  const int64_t row = blockIdx.x / p.tiles;
-  const int tile = int(blockIdx.x % p.tiles);
+  griddep_release();  // the merge may be set up
+  const int64_t row = blockIdx.x / unsigned(p.tiles);
+  const int tile = int(blockIdx.x % unsigned(p.tiles));
   const T* logits = static_cast<const T*>(p.logits) + row * p.ls;
   O* out = static_cast<O*>(p.out) + row * p.os;
   const int shift = V == 1 ? 0 : int((reinterpret_cast<uintptr_t>(logits) / sizeof(T)) % V);
@@ -235,35 +279,56 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
                         p.bias_ids_i64};
   int ids_at[kIds];
   int bias_at = -1;
-  float f[NV][V];
+  Vec<T, V> x[NV];   // as loaded: a conversion here would wait for its load before the next is issued
   uint32_t bits[NV];
-  if (history) ids.load(0, history, span, ids_at);
-  if (int(threadIdx.x) < p.n_bias) bias_at = bias_ids.one(threadIdx.x, span);
+  const bool inner = first >= 0 && first + kTile <= p.vocab;
+  if (inner) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = first + (int(threadIdx.x) + i * kRowThreads) * V;
-    if (v >= 0 && v + V <= p.vocab) {
-      const Vec<T, V> x = load_vec<T, V>(logits + v);
+    for (int i = 0; i < NV; ++i) x[i] = load_vec<T, V>(logits + first + (int(threadIdx.x) + i * kRowThreads) * V);
+  } else {
 #pragma unroll
-      for (int k = 0; k < V; ++k) f[i][k] = to_f32(x.v[k]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) f[i][k] = v + k >= 0 && v + k < p.vocab ? to_f32(logits[v + k]) : -INFINITY;
-    }
-    bits[i] = kFull;
-    if (p.mask && v > -V && v < p.vocab) {
-      const uint32_t* m = p.mask + row * p.ms;
-      if (shift == 0) {  // V divides 32: a vector's bits are in one word
-        bits[i] = m[v >> 5] >> (v & 31);
-      } else if (v >= 0) {
-        const int last = min(v + V, p.vocab) - 1;
-        bits[i] = m[v >> 5] >> (v & 31);
-        if ((last >> 5) != (v >> 5)) bits[i] |= m[last >> 5] << (32 - (v & 31));
+    for (int i = 0; i < NV; ++i) {
+      const int v = first + (int(threadIdx.x) + i * kRowThreads) * V;
+      if (v >= 0 && v + V <= p.vocab) {
+        x[i] = load_vec<T, V>(logits + v);
       } else {
-        bits[i] = m[0] << -v;
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          x[i].v[k] = v + k >= 0 && v + k < p.vocab ? logits[v + k] : from_f32<T>(-INFINITY);
       }
     }
   }
+  if (!p.mask) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) bits[i] = kFull;
+  } else {
+    const uint32_t* m = p.mask + row * p.ms;
+    const int words = (p.vocab + 31) >> 5;
+    if (shift == 0) {  // V divides 32: a vector's bits are in one word
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int w = (first + (int(threadIdx.x) + i * kRowThreads) * V) >> 5;
+        bits[i] = w < words ? m[w] : 0u;
+      }
+    } else {  // in one word or two
+      uint32_t next[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int w = (first + (int(threadIdx.x) + i * kRowThreads) * V) >> 5;  // -1: before the row
+        bits[i] = w >= 0 && w < words ? m[w] : 0u;
+        next[i] = w + 1 < words ? m[w + 1] : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = first + (int(threadIdx.x) + i * kRowThreads) * V;
+        // kept rotated, as a whole word is
+        const uint32_t w = __funnelshift_r(bits[i], next[i], v & 31);
+        bits[i] = __funnelshift_l(w, w, v & 31);
+      }
+    }
+  }
+  if (history) ids.load(0, history, span, ids_at);
+  if (int(threadIdx.x) < p.n_bias) bias_at = bias_ids.one(threadIdx.x, span);
 
   if (named) {
     constexpr int kWords = kTile + 2 * (kTile / 32) + 4;  // up to the list
@@ -280,19 +345,19 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
     // Count the history; mark what the biases name.
     for (int base = 0; base < len; base += kIdsBlock) {
       if (base) ids.load(base, len, span, ids_at);
+      uint32_t old[kIds];
+      bool any = false;
 #pragma unroll
       for (int u = 0; u < kIds; ++u) {
-        const int warp0 = base + u * kRowThreads + int(threadIdx.x & ~31u);
-        if (warp0 >= len) break;
-        const int i = warp0 + int(threadIdx.x & 31);
-        const int at = i < len ? ids_at[u] : -1;
-        bool fresh = false;
-        if (at >= 0) {
-          const uint32_t old = i < prompt ? atomicOr(&s.table[at], kPromptBit) : atomicAdd(&s.table[at], 1u);
-          fresh = old == 0;
-        }
-        append(s, at, fresh);
+        const int i = base + u * kRowThreads + int(threadIdx.x);
+        if (i >= len) ids_at[u] = -1;
+        any |= ids_at[u] >= 0;
       }
+      if (!__any_sync(kFull, any)) continue;
+#pragma unroll
+      for (int u = 0; u < kIds; ++u)
+        old[u] = count_id(&s.table[max(ids_at[u], 0)], ids_at[u] >= 0, base + u * kRowThreads + int(threadIdx.x) < prompt);
+      append(s, ids_at, old);
     }
     for (int i = threadIdx.x; i < p.n_bias; i += kRowThreads) {
       const int at = i < kRowThreads ? bias_at : bias_ids.one(i, span);
@@ -324,10 +389,15 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
           const int at = i < kRowThreads ? bias_at : bias_ids.one(i, span);
           if (at >= 0) add(at, bias[i]);
         }
-      } else if (threadIdx.x == 0) {  // in the list's order
-        for (int i = 0; i < p.n_bias; ++i) {
+      } else {  // some entry has several: their sum, in the list's order, once
+        for (int i = threadIdx.x >> 5; i < p.n_bias; i += kRowWarps) {
           const int at = bias_ids.one(i, span);
-          if (at >= 0) add(at, bias[i]);
+          if (at < 0) continue;
+          bool first_one = true;
+          for (int j = threadIdx.x & 31; j < i; j += 32) first_one &= bias_ids.one(j, span) != at;
+          if (!__all_sync(kFull, first_one)) continue;
+          const float sum = bias_sum(bias_ids, bias, p.n_bias, first + at);
+          if ((threadIdx.x & 31) == 0) add(at, sum);
         }
       }
       __syncthreads();
@@ -338,10 +408,14 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
   // entries it is, the merge looks up in `out`.
   float top = -INFINITY;
   int at_top = INT32_MAX;
+  float f[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int at = (int(threadIdx.x) + i * kRowThreads) * V;
     const int v = first + at;
+    const uint32_t allowed = __funnelshift_r(bits[i], bits[i], v & 31);  // rotated: bit k for entry v + k
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[i][k] = to_f32(x[i].v[k]);
     if (named) {
       const uint32_t w = s.map[at >> 5] >> (at & 31);
       if (w & ((1u << V) - 1)) {
@@ -354,7 +428,7 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
     float t = -INFINITY;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      if (!((bits[i] >> k) & 1u)) f[i][k] = -INFINITY;
+      if (!((allowed >> k) & 1u)) f[i][k] = -INFINITY;
       o.v[k] = from_f32<O>(f[i][k]);
       f[i][k] = to_f32(o.v[k]);
     }
@@ -369,7 +443,7 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
       top = t;
       at_top = v;
     }
-    if (v >= 0 && v + V <= p.vocab) {
+    if (inner || (v >= 0 && v + V <= p.vocab)) {
       store_vec<O, V>(out + v, o);
     } else {
 #pragma unroll
@@ -420,6 +494,7 @@ __global__ void __launch_bounds__(kRowThreads) merge_logits_kernel(const Partial
                                                                   int64_t* token, float* lse) {
   const int64_t row = blockIdx.x * int64_t(kRowWarps) + (threadIdx.x >> 5);
   if (row >= rows) return;
+  griddep_wait();  // the tiles' statistics are there
   const int lane = threadIdx.x & 31;
   Stat st;
   for (int i = lane; i < tiles; i += 32) {
@@ -466,7 +541,7 @@ int64_t plan_tiles(int64_t rows, int64_t vocab) {
 int validate(const flce_logits_problem* p) {
   if (!p) return FLCE_ERR_INVALID_ARG;
   if (p->rows < 0 || p->vocab < 1 || p->vocab > (int64_t(1) << 30)) return FLCE_ERR_INVALID_ARG;
-  if (p->history < 0 || p->history > kCountMask || p->n_bias < 0 || p->n_bias > INT32_MAX - 32)
+  if (p->history < 0 || p->history > kMaxIds || p->n_bias < 0 || p->n_bias > kMaxIds)
     return FLCE_ERR_INVALID_ARG;
   if (p->rows > INT32_MAX / plan_tiles(p->rows, p->vocab)) return FLCE_ERR_INVALID_ARG;
   if (p->logits_stride < 0 || p->tokens_stride < 0 || p->bias_ids_stride < 0 || p->bias_stride < 0 ||
@@ -525,12 +600,27 @@ cudaError_t launch_types(const LogitsParams& p, int64_t rows, const Form& f, cud
   return cudaErrorInvalidValue;
 }
 
+// As a programmatic dependent of the kernel before it on the stream (see
+// griddep_wait in the merge).
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, cudaStream_t st, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 template <class O>
 cudaError_t launch_merge(const LogitsParams& q, int64_t rows, const Form& f, int64_t* token, float* lse,
                          cudaStream_t st) {
-  merge_logits_kernel<O><<<unsigned(cdiv(rows, kRowWarps)), kRowThreads, 0, st>>>(
-      q.part, rows, q.tiles, static_cast<const O*>(q.out), q.os, q.vocab, f.vec, token, lse);
-  return cudaGetLastError();
+  return launch_dependent(merge_logits_kernel<O>, unsigned(cdiv(rows, kRowWarps)), kRowThreads, st,
+                          static_cast<const Partial*>(q.part), rows, q.tiles, static_cast<const O*>(q.out), q.os,
+                          q.vocab, f.vec, token, lse);
 }
 
 }  // namespace
