@@ -3,24 +3,36 @@
 //
 //   norm = sqrt(sum g^2),  c = min(1, max_norm / (norm + 1e-6)),  out = rn(g c)
 //
-// Two passes over the gradients, both bound by memory.  The tensors' pointers
+// Two passes over the gradients, both bound by memory (the second may find the
+// end of what the first read in L2, so it goes backwards).  The tensors' pointers
 // and sizes travel in the kernels' parameters (no copy to the device, nothing
-// for the caller to keep), and the tensors are cut into chunks that the blocks
-// take in turn, so that many small tensors cost no more than a few large ones.
+// for the caller to keep), and the tensors of a type are cut into chunks of one
+// size, a block each, so that many small tensors cost no more than a few large
+// ones and blocks go where earlier ones end.
+//
+// fp64 is slow on this part (two lanes per SM and clock): with an fp64 addition
+// per 32 elements and fp64 sums over the block the first pass ran at half the
+// memory's rate.  So a chunk is summed in fp32, compensated over its rounds, and
+// only chunks whose squares leave fp32's safe range are summed again in fp64.
 #include <algorithm>
 #include <cmath>
 
+#include "flce_device.cuh"
 #include "flce_elem.cuh"
 #include "flce_host.h"
 
 namespace flce {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kChunk = 8192;          // elements per chunk
-constexpr int kMaxGrid = 1024;        // blocks of a launch at most: partial sums per launch
+constexpr int kGradThreads = 256;
+constexpr int kTotalThreads = 1024;
+constexpr int kUnroll = 4;            // 16-byte loads under way per thread
+constexpr int kMinChunk = 8192;       // elements per chunk: this times a power of two,
+constexpr int64_t kWantChunks = 8000; // so that there are about this many at most
+constexpr int kMaxGrid = 32768;       // blocks of a launch at most: partial sums per launch
+constexpr int kFewParts = 512;       // up to here every block of the second pass adds the partial sums itself
 constexpr int kSmallTable = 32;       // tensors per launch: the small table is copied faster
-constexpr int kLargeTable = 960;      // (28.9 KB of the 32 KB of kernel parameters)
+constexpr int kLargeTable = 960;      // (27.9 KB of the 32 KB of kernel parameters)
 
 // One launch's tensors: chunk_end[i] is the number of chunks of tensors 0..i.
 template <int N>
@@ -29,9 +41,9 @@ struct GradTable {
   void* dst[N];
   int64_t numel[N];
   int32_t chunk_end[N];
-  uint8_t dtype[N];
   int32_t count;
   int32_t chunks;
+  int32_t chunk;  // elements
 };
 
 template <int N>
@@ -44,92 +56,186 @@ __device__ __forceinline__ int find_tensor(const GradTable<N>& t, int chunk) {
   return lo;
 }
 
-// Sum of squares of up to 8 values: in fp32 where that is safe, in fp64 where a
-// square could overflow fp32 or the sum is so small that squares may have
-// underflowed (fp32 squares vanish below about 1e-23; 2^-100 leaves 24 bits of
-// head-room above the subnormals for every term that matters to the sum).
-template <int V>
-__device__ __forceinline__ double sum_squares(const float (&x)[V]) {
-  float s = 0.f;
+// Sum of the squares of N values in fp32.  *safe is cleared where a square may
+// have overflowed, or the sum is so small that squares may have underflowed
+// (fp32 squares vanish below about 1e-23; 2^-100 leaves 24 bits of head-room
+// above the subnormals for every term that matters to the sum).
+template <int N>
+__device__ __forceinline__ float sum_squares(const float (&x)[N], bool* safe) {
+  constexpr int kChains = N < 8 ? N : 8;
+  float s[kChains];
 #pragma unroll
-  for (int k = 0; k < V; ++k) s = fmaf(x[k], x[k], s);
-  if (s > 0x1p-100f && s < INFINITY) return double(s);
-  double d = 0.0;
-  bool any = false;
+  for (int k = 0; k < kChains; ++k) s[k] = x[k] * x[k];
 #pragma unroll
-  for (int k = 0; k < V; ++k) any |= x[k] != 0.f;  // a NaN is not 0 either
-  if (any) {
+  for (int k = kChains; k < N; ++k) s[k % kChains] = fmaf(x[k], x[k], s[k % kChains]);
 #pragma unroll
-    for (int k = 0; k < V; ++k) d = fma(double(x[k]), double(x[k]), d);
+  for (int w = kChains / 2; w > 0; w /= 2)
+#pragma unroll
+    for (int k = 0; k < w; ++k) s[k] += s[k + w];
+  if (!(s[0] > 0x1p-100f && s[0] < 0x1p100f)) {
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < N; ++k) any |= x[k] != 0.f;  // a NaN is not 0 either
+    if (any) *safe = false;
   }
-  return d;
+  return s[0];
 }
 
-constexpr int kVec = 8;
+// A sum that keeps what its additions round off.
+struct Compensated {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = hi + x, b = t - hi;
+    lo += (hi - (t - b)) + (x - b);
+    hi = t;
+  }
+};
 
 template <class T>
-__device__ __forceinline__ double chunk_norm(const T* p, int n) {
-  double sum = 0.0;
-  const bool vec = reinterpret_cast<uintptr_t>(p) % 16 == 0;
-  const int full = vec ? n / kVec * kVec : 0;
-  for (int i = threadIdx.x * kVec; i < full; i += kThreads * kVec) {
-    const Vec<T, kVec> v = load_vec<T, kVec>(p + i);
+struct Loads {
+  static constexpr int kVec = 16 / sizeof(T);                   // elements per load
+  static constexpr int kRound = kGradThreads * kVec * kUnroll;  // elements a block has under way
+};
+// Elements before the first 16-byte boundary.
+template <class T>
+__device__ __forceinline__ int head_of(const T* p, int n) {
+  return min(n, int((16 - reinterpret_cast<uintptr_t>(p) % 16) % 16 / sizeof(T)));
+}
+
+template <class T>
+__device__ __forceinline__ float chunk_norm(const T* p, int n, bool* safe) {
+  constexpr int kVec = Loads<T>::kVec, kRound = Loads<T>::kRound;
+  Compensated sum;
+  const int head = head_of(p, n);
+  const T* q = p + head;
+  const int m = n - head, full = m / kRound * kRound;
+  for (int base = threadIdx.x * kVec; base < full; base += kRound) {
+    Vec<T, kVec> v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) v[u] = load_vec<T, kVec>(q + base + u * kGradThreads * kVec);
+    float x[kUnroll * kVec];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) x[u * kVec + k] = to_f32(v[u].v[k]);
+    sum.add(sum_squares(x, safe));
+  }
+  int i = full + threadIdx.x * kVec;
+  for (; i + kVec <= m; i += kGradThreads * kVec) {
+    const Vec<T, kVec> v = load_vec<T, kVec>(q + i);
     float x[kVec];
 #pragma unroll
     for (int k = 0; k < kVec; ++k) x[k] = to_f32(v.v[k]);
-    sum += sum_squares<kVec>(x);
+    sum.add(sum_squares(x, safe));
   }
-  for (int i = full + threadIdx.x; i < n; i += kThreads) {
-    const float x[1] = {to_f32(p[i])};
-    sum += sum_squares<1>(x);
+  // what is left: the head, and less than a vector at the end
+  const int tail = full + (m - full) / kVec * kVec;
+  for (i = threadIdx.x; i < head + m - tail; i += kGradThreads) {
+    const float x[1] = {to_f32(i < head ? p[i] : q[tail + i - head])};
+    sum.add(sum_squares(x, safe));
   }
-  return sum;
+  return sum.hi + sum.lo;
 }
 
-template <int N>
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ GradTable<N> t, double* part) {
-  __shared__ double red[32];
-  double sum = 0.0;
+// Sum over the block in fp64 with as few additions as there are values (a
+// butterfly would make every lane add); every thread gets it.
+__device__ __forceinline__ double block_tree(double x, double* red) {
+  __syncthreads();  // `red` may still be read from the call before
+  red[threadIdx.x] = x;
+  for (int w = blockDim.x / 2; w > 0; w /= 2) {
+    __syncthreads();
+    if (int(threadIdx.x) < w) red[threadIdx.x] += red[threadIdx.x + w];
+  }
+  __syncthreads();
+  return red[0];
+}
+
+template <int N, class T>
+__global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_constant__ GradTable<N> t, double* part) {
+  __shared__ double red[kGradThreads];
+  __shared__ float red32[32];
+  griddep_release();  // the next kernel may be set up
+  double all = 0.0;
   for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     const int i = find_tensor(t, c);
-    const int64_t begin = int64_t(c - (i ? t.chunk_end[i - 1] : 0)) * kChunk;
-    const int n = int(min(int64_t(kChunk), t.numel[i] - begin));
-    if (t.dtype[i] == FLCE_F32) {
-      sum += chunk_norm(static_cast<const float*>(t.src[i]) + begin, n);
-    } else if (t.dtype[i] == FLCE_BF16) {
-      sum += chunk_norm(static_cast<const __nv_bfloat16*>(t.src[i]) + begin, n);
+    const int64_t begin = int64_t(c - (i ? t.chunk_end[i - 1] : 0)) * t.chunk;
+    const int n = int(min(int64_t(t.chunk), t.numel[i] - begin));
+    const T* p = static_cast<const T*>(t.src[i]) + begin;
+    bool safe = true;
+    float s = chunk_norm(p, n, &safe);
+    if (!__syncthreads_or(!safe)) {
+      s = block_sum(s, red32);
+      all += double(s);
     } else {
-      sum += chunk_norm(static_cast<const __half*>(t.src[i]) + begin, n);
+      double d = 0.0;
+      for (int k = threadIdx.x; k < n; k += kGradThreads) {
+        const double x = double(to_f32(p[k]));
+        d = fma(x, x, d);
+      }
+      all += block_tree(d, red);
     }
   }
-  sum = block_sum(sum, red);
-  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+  if (threadIdx.x == 0) part[blockIdx.x] = all;
 }
 
-// Sum of the blocks' partial sums, the same in every block.
+// Sum of the blocks' partial sums; `red` has blockDim.x values.
 __device__ __forceinline__ double total(const double* part, int n, double* red) {
   double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) s += part[i];
-  return block_sum(s, red);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += blockDim.x) s += part[i];
+  return block_tree(s, red);
 }
 
-__global__ void __launch_bounds__(kThreads) norm_total_kernel(const double* part, int n, float* norm) {
-  __shared__ double red[32];
+__global__ void __launch_bounds__(kTotalThreads) norm_total_kernel(const double* part, int n, float* norm) {
+  __shared__ double red[kTotalThreads];
+  griddep_release();
+  griddep_wait();  // the partial sums are there
   const double s = total(part, n, red);
   if (threadIdx.x == 0) *norm = float(sqrt(s));
 }
 
 template <class T>
 __device__ __forceinline__ void chunk_scale(const T* src, T* dst, int n, float c) {
-  const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && reinterpret_cast<uintptr_t>(dst) % 16 == 0;
-  const int full = vec ? n / kVec * kVec : 0;
-  for (int i = threadIdx.x * kVec; i < full; i += kThreads * kVec) {
-    Vec<T, kVec> v = load_vec<T, kVec>(src + i);
+  constexpr int kVec = Loads<T>::kVec, kRound = Loads<T>::kRound;
+  // 16-byte loads and stores where both sides reach a boundary together
+  if ((reinterpret_cast<uintptr_t>(src) - reinterpret_cast<uintptr_t>(dst)) % 16 == 0) {
+    const int head = head_of(src, n), m = n - head;
+    const T* q = src + head;
+    T* o = dst + head;
+    for (int base = threadIdx.x * kVec; base < m; base += kRound) {
+      Vec<T, kVec> v[kUnroll];
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) v.v[k] = from_f32<T>(to_f32(v.v[k]) * c);
-    store_vec<T, kVec>(dst + i, v);
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = base + u * kGradThreads * kVec;
+        if (i + kVec <= m) v[u] = load_vec<T, kVec>(q + i);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = base + u * kGradThreads * kVec;
+        if (i + kVec <= m) {
+#pragma unroll
+          for (int k = 0; k < kVec; ++k) v[u].v[k] = from_f32<T>(to_f32(v[u].v[k]) * c);
+          store_vec<T, kVec>(o + i, v[u]);
+        }
+      }
+    }
+    const int tail = m / kVec * kVec;
+    for (int i = threadIdx.x; i < head + m - tail; i += kGradThreads) {
+      const int at = i < head ? i : head + tail + i - head;
+      dst[at] = from_f32<T>(to_f32(src[at]) * c);
+    }
+    return;
   }
-  for (int i = full + threadIdx.x; i < n; i += kThreads) dst[i] = from_f32<T>(to_f32(src[i]) * c);
+  constexpr int kSingles = 16;  // loads under way
+  for (int base = threadIdx.x; base < n; base += kGradThreads * kSingles) {
+    T x[kSingles];
+#pragma unroll
+    for (int u = 0; u < kSingles; ++u)
+      if (base + u * kGradThreads < n) x[u] = src[base + u * kGradThreads];
+#pragma unroll
+    for (int u = 0; u < kSingles; ++u)
+      if (base + u * kGradThreads < n) dst[base + u * kGradThreads] = from_f32<T>(to_f32(x[u]) * c);
+  }
 }
 
 // min(1, max / (norm + 1e-6)) that keeps a NaN.
@@ -138,13 +244,21 @@ __device__ __forceinline__ float clip_factor(float norm, float max_norm) {
   return c > 1.0f ? 1.0f : c;
 }
 
-template <int N>
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ GradTable<N> t,
+template <int N, class T>
+__global__ void __launch_bounds__(kGradThreads, 4) grad_scale_kernel(const __grid_constant__ GradTable<N> t,
                                                              const double* part, int n_part, float max_norm,
                                                              float* norm) {
-  __shared__ double red[32];
-  const float nm = float(sqrt(total(part, n_part, red)));
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = nm;
+  // n_part > 0: the norm is still to be added up, else *norm has it
+  __shared__ double red[kGradThreads];
+  griddep_release();
+  griddep_wait();  // the partial sums, or the norm, are there
+  float nm;
+  if (n_part > 0) {
+    nm = float(sqrt(total(part, n_part, red)));
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = nm;
+  } else {
+    nm = *norm;
+  }
   const float f = clip_factor(nm, max_norm);
   // an infinite limit over an infinite norm is NaN; such a limit clips nothing
   const float c = max_norm == INFINITY && nm == nm ? 1.0f : f;
@@ -152,23 +266,16 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
   for (int c0 = t.chunks - 1 - int(blockIdx.x); c0 >= 0; c0 -= gridDim.x) {
     const int i = find_tensor(t, c0);
     if (c == 1.0f && t.src[i] == t.dst[i]) continue;
-    const int64_t begin = int64_t(c0 - (i ? t.chunk_end[i - 1] : 0)) * kChunk;
-    const int n = int(min(int64_t(kChunk), t.numel[i] - begin));
-    if (t.dtype[i] == FLCE_F32) {
-      chunk_scale(static_cast<const float*>(t.src[i]) + begin, static_cast<float*>(t.dst[i]) + begin, n, c);
-    } else if (t.dtype[i] == FLCE_BF16) {
-      chunk_scale(static_cast<const __nv_bfloat16*>(t.src[i]) + begin, static_cast<__nv_bfloat16*>(t.dst[i]) + begin,
-                  n, c);
-    } else {
-      chunk_scale(static_cast<const __half*>(t.src[i]) + begin, static_cast<__half*>(t.dst[i]) + begin, n, c);
-    }
+    const int64_t begin = int64_t(c0 - (i ? t.chunk_end[i - 1] : 0)) * t.chunk;
+    const int n = int(min(int64_t(t.chunk), t.numel[i] - begin));
+    chunk_scale(static_cast<const T*>(t.src[i]) + begin, static_cast<T*>(t.dst[i]) + begin, n, c);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-constexpr int64_t kMaxChunks = INT32_MAX / 2;  // of all tensors together: 8.8e12 elements
+constexpr int64_t kMaxElements = int64_t(1) << 42;  // of all tensors together
 
 struct Grads {
   const void* const* src;
@@ -181,12 +288,12 @@ struct Grads {
 int validate(const Grads& g, bool clip) {
   if (g.count < 0 || g.count > (int64_t(1) << 24)) return FLCE_ERR_INVALID_ARG;
   if (g.count > 0 && (!g.src || !g.numel || !g.dtypes || (clip && !g.dst))) return FLCE_ERR_INVALID_ARG;
-  int64_t chunks = 0;
+  int64_t elements = 0;
   for (int64_t i = 0; i < g.count; ++i) {
     if (!known_dtype(g.dtypes[i])) return FLCE_ERR_UNSUPPORTED_DTYPE;
-    if (g.numel[i] < 0 || g.numel[i] / kChunk >= kMaxChunks) return FLCE_ERR_INVALID_ARG;
-    chunks += (g.numel[i] + kChunk - 1) / kChunk;
-    if (chunks > kMaxChunks) return FLCE_ERR_INVALID_ARG;
+    if (g.numel[i] < 0 || g.numel[i] > kMaxElements) return FLCE_ERR_INVALID_ARG;
+    elements += g.numel[i];
+    if (elements > kMaxElements) return FLCE_ERR_INVALID_ARG;
     if (g.numel[i] == 0) continue;
     if (!g.src[i] || (clip && !g.dst[i])) return FLCE_ERR_INVALID_ARG;
     const size_t e = elem_size(g.dtypes[i]);
@@ -195,56 +302,62 @@ int validate(const Grads& g, bool clip) {
   return FLCE_OK;
 }
 
-// Fills `t` with tensors from index *next on, as many as fit.
+// Fills `t` with tensors of a type from index *next on, as many as fit.
 template <int N>
-void fill(GradTable<N>& t, const Grads& g, int64_t* next) {
+void fill(GradTable<N>& t, const Grads& g, int32_t dtype, int64_t* next, int32_t chunk) {
   t.count = 0;
   t.chunks = 0;
+  t.chunk = chunk;
   for (; *next < g.count && t.count < N; ++*next) {
     const int64_t i = *next;
-    if (g.numel[i] == 0) continue;
+    if (g.numel[i] == 0 || g.dtypes[i] != dtype) continue;
     t.src[t.count] = g.src[i];
     t.dst[t.count] = g.dst ? g.dst[i] : nullptr;
     t.numel[t.count] = g.numel[i];
-    t.dtype[t.count] = uint8_t(g.dtypes[i]);
-    t.chunks += int32_t((g.numel[i] + kChunk - 1) / kChunk);
+    t.chunks += int32_t((g.numel[i] + chunk - 1) / chunk);
     t.chunk_end[t.count++] = t.chunks;
   }
 }
 
-int grid_for(int chunks, int num_sms) { return std::max(1, std::min({chunks, 4 * num_sms, kMaxGrid})); }
+// Calls launch(table, type) for tables that hold all tensors.
+template <int N, class F>
+int for_tables(const Grads& g, int32_t chunk, cudaStream_t st, F&& launch) {
+  GradTable<N> t;
+  auto of = [&](int32_t dtype, auto type) {
+    for (int64_t next = 0; next < g.count;) {
+      fill(t, g, dtype, &next, chunk);
+      if (t.count) FLCE_TRY(logged(FLCE_LAUNCH_OTHER, st, [&] { return launch(t, type); }));
+    }
+    return int(FLCE_OK);
+  };
+  FLCE_TRY(of(FLCE_F32, float()));
+  FLCE_TRY(of(FLCE_BF16, __nv_bfloat16()));
+  return of(FLCE_F16, __half());
+}
 
 template <int N>
-int run_tables(const Grads& g, bool clip, float max_norm, float* norm, double* part, int num_sms, cudaStream_t st) {
-  GradTable<N> t;
+int run_tables(const Grads& g, bool clip, float max_norm, float* norm, double* part, cudaStream_t st) {
+  int64_t elements = 0;
+  for (int64_t i = 0; i < g.count; ++i) elements += g.numel[i];
+  int32_t chunk = kMinChunk;  // at most 2^30 elements, for 2^42
+  while (elements / chunk > kWantChunks) chunk *= 2;
   int parts = 0;
-  for (int64_t next = 0; next < g.count;) {
-    fill(t, g, &next);
-    if (t.count == 0) continue;  // only empty tensors were left
-    const int grid = grid_for(t.chunks, num_sms);
-    FLCE_TRY(logged(FLCE_LAUNCH_OTHER, st, [&] {
-      grad_norm_kernel<N><<<grid, kThreads, 0, st>>>(t, part + parts);
-      return cudaGetLastError();
-    }));
+  FLCE_TRY(for_tables<N>(g, chunk, st, [&](const GradTable<N>& t, auto type) {
+    const int grid = std::min(t.chunks, kMaxGrid);
+    grad_norm_kernel<N, decltype(type)><<<grid, kGradThreads, 0, st>>>(t, part + parts);
     parts += grid;
-  }
-  if (!clip || parts == 0)
-    return logged(FLCE_LAUNCH_OTHER, st, [&] {
-      norm_total_kernel<<<1, kThreads, 0, st>>>(part, parts, norm);
-      return cudaGetLastError();
-    });
-  bool first = true;
-  for (int64_t next = 0; next < g.count;) {
-    fill(t, g, &next);
-    if (t.count == 0) continue;
+    return cudaGetLastError();
+  }));
+  const bool alone = !clip || parts == 0 || parts > kFewParts;
+  if (alone)
     FLCE_TRY(logged(FLCE_LAUNCH_OTHER, st, [&] {
-      grad_scale_kernel<N><<<grid_for(t.chunks, num_sms), kThreads, 0, st>>>(t, part, parts, max_norm,
-                                                                            first ? norm : nullptr);
-      return cudaGetLastError();
+      return launch_dependent(norm_total_kernel, 1, kTotalThreads, st, static_cast<const double*>(part), parts, norm);
     }));
-    first = false;
-  }
-  return FLCE_OK;
+  if (!clip || parts == 0) return FLCE_OK;
+  return for_tables<N>(g, chunk, st, [&](const GradTable<N>& t, auto type) {
+    return launch_dependent(grad_scale_kernel<N, decltype(type)>, unsigned(std::min(t.chunks, kMaxGrid)), kGradThreads,
+                            st, t, static_cast<const double*>(part), alone ? 0 : parts, max_norm, norm);
+  });
 }
 
 int run(const Grads& g, bool clip, float max_norm, float* norm, void* workspace, size_t workspace_bytes,
@@ -265,8 +378,8 @@ int run(const Grads& g, bool clip, float max_norm, float* norm, void* workspace,
   }
   double* part = static_cast<double*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return g.count <= kSmallTable ? run_tables<kSmallTable>(g, clip, max_norm, norm, part, dev.num_sms, st)
-                                : run_tables<kLargeTable>(g, clip, max_norm, norm, part, dev.num_sms, st);
+  return g.count <= kSmallTable ? run_tables<kSmallTable>(g, clip, max_norm, norm, part, st)
+                                : run_tables<kLargeTable>(g, clip, max_norm, norm, part, st);
 }
 
 }  // namespace
@@ -278,9 +391,8 @@ extern "C" {
 
 int flce_grad_norm_workspace_size(int64_t count, size_t* bytes) {
   if (!bytes || count < 0 || count > (int64_t(1) << 24)) return FLCE_ERR_INVALID_ARG;
-  // one partial sum per block and launch
-  const int64_t launches = std::max<int64_t>(1, (count + kLargeTable - 1) / kLargeTable);
-  *bytes = size_t(launches) * kMaxGrid * sizeof(double);
+  // one partial sum per block: at most kWantChunks + one for each tensor
+  *bytes = size_t(kWantChunks + count + 32) * sizeof(double);
   return FLCE_OK;
 }
 

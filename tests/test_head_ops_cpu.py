@@ -115,8 +115,8 @@ def test_clip_refusals(lib):
     assert lib.flce_grad_norm_workspace_size(3, None) == inv
     assert lib.flce_grad_norm_workspace_size(2, ctypes.byref(n)) == B.FLCE_OK
     ws = n.value
-    # one partial sum for each block of each launch, and more launches for more tensors
-    assert lib.flce_grad_norm_workspace_size(100000, ctypes.byref(n)) == B.FLCE_OK and n.value >= 100 * ws
+    # partial sums: at least one for each tensor
+    assert lib.flce_grad_norm_workspace_size(100000, ctypes.byref(n)) == B.FLCE_OK and n.value >= 100000 * 8
 
     def clip(g, max_norm=1.0, norm=_a(30), w=_a(31), size=ws, count=2):
         return lib.flce_clip_grad_norm(g[0], g[1], g[2], g[3], count, max_norm, norm, w, size, None)
