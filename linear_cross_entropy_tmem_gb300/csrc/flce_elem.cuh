@@ -86,6 +86,22 @@ __device__ __forceinline__ F block_sum(F x, F* buf) {
   return warp_sum(lane < warps ? buf[lane] : F(0));
 }
 
+// As a programmatic dependent of the kernel before it on the stream (it
+// may start while that one finishes, and waits for it in griddep_wait).
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, cudaStream_t st, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 inline size_t elem_size(int32_t dtype) { return dtype == FLCE_F32 ? 4 : 2; }
 inline bool known_dtype(int32_t dtype) { return dtype == FLCE_F32 || dtype == FLCE_BF16 || dtype == FLCE_F16; }
 inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }

@@ -600,21 +600,6 @@ cudaError_t launch_types(const LogitsParams& p, int64_t rows, const Form& f, cud
   return cudaErrorInvalidValue;
 }
 
-// As a programmatic dependent of the kernel before it on the stream (see
-// griddep_wait in the merge).
-template <class... P, class... A>
-cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, cudaStream_t st, A... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
 template <class O>
 cudaError_t launch_merge(const LogitsParams& q, int64_t rows, const Form& f, int64_t* token, float* lse,
                          cudaStream_t st) {
