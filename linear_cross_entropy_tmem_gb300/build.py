@@ -1,8 +1,9 @@
-"""In-tree build of ``libflce.so`` for sm_103a with nvcc (no cmake, no setuptools).
+"""In-tree build of ``libflce.so`` for sm_103a with nvcc (no cmake, no setuptools), and of ``flce_torch.so``, the
+native marshalling of torch tensors, with the host compiler.
 
-The translation units compile in parallel; the library is relinked only
-when a source or header is newer than it.  Output:
-``linear_cross_entropy_tmem_gb300/_build/libflce.so``.
+The translation units compile in parallel; the outputs are rebuilt only when a
+source or header is newer than they are.  Output:
+``linear_cross_entropy_tmem_gb300/_build/``.
 
     python -m linear_cross_entropy_tmem_gb300.build
 """
@@ -23,6 +24,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libflce.so")
 SOURCES = ["flce_api.cu", "flce_fwd.cu", "flce_bwd.cu", "flce_noalloc.cu", "flce_norm.cu", "flce_norm_fwd.cu", "flce_norm_fp8.cu",
            "flce_norm_bwd.cu", "flce_clip.cu", "flce_logits.cu"]
+TORCH_SOURCE = "flce_torch.cpp"
+TORCH_LIB = os.path.join(BUILD, "flce_torch.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -53,13 +56,37 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_torch() -> str:
+    """flce_torch.so: a Python extension on torch's C++ interface."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = TORCH_LIB + ".tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}", f"-isystem{inc}",
+           f"-isystem{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-isystem{cuda}",
+           f"-I{sysconfig.get_paths()['include']}", os.path.join(CSRC, TORCH_SOURCE), "-o", tmp, f"-L{lib}",
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {TORCH_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Build (or reuse) libflce.so and return its path."""
     os.makedirs(BUILD, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
+    newest = _newest_input()
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, TORCH_LIB)):
         return LIB
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_compile_torch)
         objs = list(ex.map(_compile, SOURCES))
+        marshal.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -8,6 +8,10 @@
 
 As in ``api.py``, PyTorch provides device memory and the current stream, every step runs in
 ``libflce.so``, and there is no CPU path.  See ``include/flce.h`` for the formulas.
+
+Tensors that are as the library wants them are marshalled by ``flce_torch.so`` (a step of one token
+is shorter than reading its tensors' fields from Python); it returns None for the others, which the
+code here views as rows, or refuses.
 """
 from __future__ import annotations
 
@@ -27,6 +31,20 @@ def _code(dt: torch.dtype, what: str) -> int:
     if code is None:
         raise TypeError(f"flce: {what}: dtype {dt} is not supported (bf16, fp16 or fp32)")
     return code
+
+
+_native = None  # flce_torch, once it is loaded
+
+
+def _call(name: str, *args):
+    """The outputs of a native call, or None where the tensors need a closer look."""
+    global _native
+    if _native is None:
+        _native = B.load_torch()
+    out = getattr(_native, name)(*args)
+    if type(out) is int:
+        raise B.FlceError(out, name)
+    return out
 
 
 def _stream(device: torch.device) -> int:
@@ -146,8 +164,10 @@ def flce_add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                       need_rstd: bool = True) -> AddRmsNormResult:
     """Forward of the residual addition and norm over the last dimension (see ``flce_add_rms_norm`` in
     include/flce.h); ``need_rstd=False`` where no backward follows."""
-    y, h, r = _norm_forward(x, weight, residual, eps, weight_offset, rstd=need_rstd)
-    return AddRmsNormResult(y, h, r)
+    out = _call("add_rms_norm", x, weight, residual, eps, weight_offset, bool(need_rstd), -1)
+    if out is None:
+        out = _norm_forward(x, weight, residual, eps, weight_offset, rstd=need_rstd)
+    return AddRmsNormResult._make(out)
 
 
 def flce_add_rms_norm_fp8(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -155,7 +175,11 @@ def flce_add_rms_norm_fp8(x: torch.Tensor, weight: Optional[torch.Tensor] = None
                           group: int = 128) -> AddRmsNormFp8Result:
     """The forward with an e4m3 output and one fp32 scale per ``group`` columns of a row (0: per row; see
     ``flce_add_rms_norm_fp8``)."""
-    q, h, s = _norm_forward(x, weight, residual, eps, weight_offset, rstd=False, group=int(group))
+    if group < 0:
+        raise ValueError(f"flce: group must not be negative, got {group}")
+    out = _call("add_rms_norm", x, weight, residual, eps, weight_offset, False, int(group))
+    q, h, s = out if out is not None else _norm_forward(x, weight, residual, eps, weight_offset, rstd=False,
+                                                        group=int(group))
     return AddRmsNormFp8Result(q, s, h)
 
 
@@ -165,6 +189,10 @@ def flce_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Te
                                need_dweight: bool = True, workspace: Optional[torch.Tensor] = None) -> AddRmsNormGrads:
     """Backward (see ``flce_add_rms_norm_backward``): ``dy`` is the gradient of y, ``dh`` that of h from its other
     uses; ``h`` and ``rstd`` come from the forward.  ``dx`` has dy's dtype, ``dresidual`` h's."""
+    out = _call("add_rms_norm_backward", dy, h, rstd, weight, dh, weight_offset, bool(need_dx), bool(need_dresidual),
+                bool(need_dweight), workspace)
+    if out is not None:
+        return AddRmsNormGrads._make(out)
     dev = dy.device
     _on(dev, dy=dy, h=h, rstd=rstd, weight=weight, dh=dh)
     if h.shape != dy.shape or (dh is not None and (dh.shape != dy.shape or dh.dtype != h.dtype)):
@@ -305,6 +333,9 @@ def _grad_workspace(n: int, dev, workspace):
 def grad_norm(grads: Iterable[torch.Tensor], *, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The 2-norm of all elements of all ``grads``, a 0-dim fp32 device tensor (see ``flce_grad_norm``)."""
     grads = list(grads)
+    out = _call("clip_grad_norm", grads, None, None, workspace)
+    if out is not None:
+        return out[0]
     dev, n, (src, _, numel, codes) = _grad_arrays(grads, None)
     ws, nbytes = _grad_workspace(n, dev, workspace)
     norm = torch.empty((), dtype=torch.float32, device=dev)
@@ -324,6 +355,9 @@ def clip_grad_norm_(grads: Iterable[torch.Tensor], max_norm: float, *,
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
         raise ValueError(f"flce: max_norm must not be negative, got {max_norm}")
+    out = _call("clip_grad_norm", grads, max_norm, outputs, workspace)
+    if out is not None:
+        return out[0]
     dev, n, (src, dst, numel, codes) = _grad_arrays(grads, outputs)
     ws, nbytes = _grad_workspace(n, dev, workspace)
     norm = torch.empty((), dtype=torch.float32, device=dev)
@@ -371,6 +405,10 @@ def process_logits(logits: torch.Tensor, *, tokens: Optional[torch.Tensor] = Non
     ``prompt_lens[b]`` are its prompt; ``repetition``, ``presence``, ``frequency`` [B] fp32.  ``bias_ids`` and
     ``bias`` [B, K]: sparse additions.  Ids outside [0, V) are padding.  ``mask`` [B, ceil(V / 32)] int32: bit
     v % 32 of word v // 32 allows entry v.  ``out`` may be ``logits``; ``out_dtype`` is logits' dtype or fp32."""
+    res = _call("process_logits", logits, tokens, lens, prompt_lens, repetition, presence, frequency, bias_ids, bias,
+                mask, out, -1 if out_dtype is None else _code(out_dtype, "out"), workspace)
+    if res is not None:
+        return ProcessedLogits._make(res)
     dev = logits.device
     _on(dev, logits=logits, tokens=tokens, lens=lens, prompt_lens=prompt_lens, repetition=repetition,
         presence=presence, frequency=frequency, bias_ids=bias_ids, bias=bias, mask=mask, out=out)
