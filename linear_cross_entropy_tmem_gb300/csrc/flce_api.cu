@@ -49,6 +49,7 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+PFN_cuPointerGetAttributes_v7000 g_attributes = nullptr;
 
 }  // namespace
 
@@ -73,6 +74,14 @@ int get_device(DeviceInfo* out) {
         q != cudaDriverEntryPointSuccess || !fn)
       return FLCE_ERR_CUDA;
     g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  if (!g_attributes) {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &fn, 7000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn)
+      return FLCE_ERR_CUDA;
+    g_attributes = reinterpret_cast<PFN_cuPointerGetAttributes_v7000>(fn);
   }
   *out = d;
   if (d.major != 10 || d.minor != 3) return FLCE_ERR_UNSUPPORTED_DEVICE;
@@ -127,6 +136,21 @@ int check_local(const DeviceInfo& dev, const void* p) {
   if (a.type == cudaMemoryTypeManaged) return FLCE_OK;
   if (a.type == cudaMemoryTypeDevice && a.device == dev.index) return FLCE_OK;
   return FLCE_ERR_INVALID_ARG;
+}
+
+int check_local(const DeviceInfo& dev, const void* p, LocalRanges* known) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  if (!p || (at >= known->begin && at < known->end)) return FLCE_OK;
+  FLCE_TRY(check_local(dev, p));
+  CUdeviceptr begin = 0;
+  size_t bytes = 0;
+  CUpointer_attribute what[2] = {CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+  void* to[2] = {&begin, &bytes};
+  // without a range the next pointer is queried again
+  if (g_attributes(2, what, to, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS) return FLCE_OK;
+  known->begin = uintptr_t(begin);
+  known->end = uintptr_t(begin) + bytes;
+  return FLCE_OK;
 }
 
 namespace {

@@ -371,10 +371,11 @@ int run(const Grads& g, bool clip, float max_norm, float* norm, void* workspace,
   DeviceInfo dev;
   FLCE_TRY(get_device(&dev));
   FLCE_TRY(check_local(dev, norm, workspace));
+  LocalRanges src, dst;
   for (int64_t i = 0; i < g.count; ++i) {
     if (g.numel[i] == 0) continue;
-    FLCE_TRY(check_local(dev, g.src[i]));
-    if (clip && g.dst[i] != g.src[i]) FLCE_TRY(check_local(dev, g.dst[i]));
+    FLCE_TRY(check_local(dev, g.src[i], &src));
+    if (clip && g.dst[i] != g.src[i]) FLCE_TRY(check_local(dev, g.dst[i], &dst));
   }
   double* part = static_cast<double*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

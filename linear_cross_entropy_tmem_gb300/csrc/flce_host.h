@@ -5,6 +5,8 @@
 
 #include <cuda_runtime.h>
 
+#include <cstdint>
+
 #include "flce.h"
 #include "flce_testing.h"
 
@@ -34,6 +36,13 @@ int check_local(const DeviceInfo& dev, const void* p, P... rest) {
   FLCE_TRY(check_local(dev, p));
   return check_local(dev, rest...);
 }
+
+// The same for many pointers of one call: one inside an allocation that the call
+// has already found local needs no query.
+struct LocalRanges {
+  uintptr_t begin = 0, end = 0;  // the last allocation found local
+};
+int check_local(const DeviceInfo& dev, const void* p, LocalRanges* known);
 
 int log_begin(cudaStream_t st, flce_launch_record** rec);
 int log_end(int kind, cudaStream_t st, flce_launch_record* rec);
