@@ -420,9 +420,7 @@ FLCE_API int flce_add_rms_norm(const flce_norm_problem* problem, const void* x, 
  * Forward whose normalised output is held in 8 bits (e4m3, largest value 448):
  * for each group of quant_group columns of a row (the last may be short)
  *   scale = max_j |y_j| / 448,  q_j = e4m3(y_j / scale), 0 where scale is 0,
- * with y in fp32, the divisions by products with reciprocals (each within two
- * units in the last place of fp32).  A group with a NaN or an infinity gets a
- * non-finite scale.
+ * with y in fp32.  A group with a NaN or an infinity gets a non-finite scale.
  *   q      [N, D] bytes, y_stride between rows
  *   scale  [N, ceil(D / group)] fp32, dense
  */

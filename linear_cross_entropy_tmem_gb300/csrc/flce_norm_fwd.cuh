@@ -9,20 +9,24 @@
 namespace flce {
 namespace {
 
-// What a group's values are multiplied with: 1 / s, 0 where s is 0.  Below 2^-100
-// (where 1 / s may overflow) the values take a factor of 2^64 first.
+// Division by a group's scale: y times the reciprocal, and one step that makes
+// up for its rounding, so that q is e4m3 of the quotient as rounded to fp32.
+// Below 2^-100 (where 1 / s may overflow) values take a factor of 2^64 first.
 struct Inverse {
-  float first, inv;
+  float first, inv, minus;  // minus: -s, or 0 where the step would make NaN of 0
 };
 __device__ __forceinline__ Inverse inverse_of(float s) {
-  if (s >= 0x1p-100f || s != s) return {1.0f, __frcp_rn(s)};
-  return {0x1p64f, s == 0.0f ? 0.0f : __frcp_rn(s * 0x1p64f)};
+  const bool small = s < 0x1p-100f;
+  if (small) s *= 0x1p64f;
+  const float inv = s == 0.f ? 0.f : __frcp_rn(s);
+  return {small ? 0x1p64f : 1.0f, inv, s < INFINITY ? -s : 0.f};
 }
-// amax / 448 by a constant's product: within one unit in the last place.
-__device__ __forceinline__ float scale_of(uint32_t amax_bits) { return __uint_as_float(amax_bits) * (1.0f / kE4m3Max); }
+__device__ __forceinline__ float scale_of(uint32_t amax_bits) { return __uint_as_float(amax_bits) / kE4m3Max; }
 // e4m3(y / s); saturates, NaN stays NaN.
 __device__ __forceinline__ uint8_t quantise(float y, const Inverse& i) {
-  return uint8_t(__nv_cvt_float_to_fp8(y * i.first * i.inv, __NV_SATFINITE, __NV_E4M3));
+  y *= i.first;
+  const float q = y * i.inv;
+  return uint8_t(__nv_cvt_float_to_fp8(fmaf(fmaf(q, i.minus, y), i.inv, q), __NV_SATFINITE, __NV_E4M3));
 }
 
 // The largest of |a|, |b|, |c|, a NaN if any is one.
@@ -160,8 +164,9 @@ __global__ void __launch_bounds__(row_threads(kForm), fwd_blocks(kForm, kRagged)
             Vec<uint8_t, V> qv;
 #pragma unroll
             for (int j = 0; j < v[i].kPairs; ++j) {
+              const uint64_t i2 = f2_splat(inv.inv), quo = f2_mul(v[i].p[j], i2);
               float2 y;
-              f2_unpack(f2_mul(v[i].p[j], f2_splat(inv.inv)), y.x, y.y);
+              f2_unpack(f2_fma(f2_fma(quo, f2_splat(inv.minus), v[i].p[j]), i2, quo), y.x, y.y);
               if constexpr (V > 1)
                 *reinterpret_cast<__nv_fp8x2_storage_t*>(&qv.v[2 * j]) =
                     __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
