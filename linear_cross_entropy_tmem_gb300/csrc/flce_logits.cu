@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
   Span span;
   span.first = tile * kTile - shift;  // < 0 in a shifted first tile
   span.begin = max(span.first, 0);
-  span.count = min(span.first + kTile, p.vocab) - span.begin;
+  span.count = max(0, min(span.first + kTile, p.vocab) - span.begin);  // 0: the row ends before the tile
   const int first = span.first;
 
   // The loads of the lists and of the tile go out together.  The first ids are
@@ -371,10 +371,22 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
     // One thread per listed place works out its value from the logit (in L1:
     // the tile's loads have just passed there).
     const int n = s.n_list;
-    for (int i = threadIdx.x; i < n; i += kRowThreads) {
-      const int at = s.list[i];
-      s.table[at] = __float_as_uint(penalise(to_f32(logits[first + at]), s.table[at], rep, pres, freq, has_rep));
-      mark(s.map, at);
+    constexpr int kLoads = 4;  // under way at once
+    for (int base = threadIdx.x; base < n; base += kRowThreads * kLoads) {
+      int at[kLoads];
+      float z[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const int i = base + u * kRowThreads;
+        at[u] = i < n ? int(s.list[i]) : -1;
+        if (at[u] >= 0) z[u] = to_f32(logits[first + at[u]]);
+      }
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+        if (at[u] >= 0) {
+          s.table[at[u]] = __float_as_uint(penalise(z[u], s.table[at[u]], rep, pres, freq, has_rep));
+          mark(s.map, at[u]);
+        }
     }
     __syncthreads();
     if (s.biased) {
@@ -568,7 +580,8 @@ Form plan_form(const flce_logits_problem* p, const void* logits, const void* out
   f.vec = ok ? wide : 1;
   const int per = plan_per_thread(p->rows, p->vocab);
   f.nv = f.vec == 1 ? std::min(kMaxSingles, per) : std::max(1, per / f.vec);
-  f.tiles = int32_t(cdiv(p->vocab + f.vec - 1, int64_t(kRowThreads) * f.vec * f.nv));
+  const bool shifted = a % f.vec != 0 || (p->rows > 1 && p->logits_stride % f.vec != 0);
+  f.tiles = int32_t(cdiv(p->vocab + (shifted ? f.vec - 1 : 0), int64_t(kRowThreads) * f.vec * f.nv));
   return f;
 }
 

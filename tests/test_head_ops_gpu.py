@@ -536,6 +536,31 @@ def test_logits_history_lengths_and_padding():
     check_logits(z, **kw)
 
 
+@pytest.mark.parametrize("t", [SP, HF])
+@pytest.mark.parametrize("v", [1021, 2046, 2047, 2048, 4093, 8185, 8190, 8191, 8192])
+def test_logits_padding_beyond_a_vocabulary_that_ends_near_a_tile(t, v):
+    """Ids at and far beyond the vocabulary are padding also where the last tile has few entries or none, for
+    histories of one round and of several."""
+    for h in (40, 1500):
+        kw = options(2, v, h, 6, v)
+        pad = torch.tensor([v, v + 1, v + 7, v + 8192, 2 ** 31 - 1, -1, 2 ** 40], device="cuda")
+        kw["tokens"][:, 3:3 + len(pad)] = pad
+        kw["bias_ids"][:, :2] = pad[2:4]
+        kw["lens"][:] = h
+        check_logits(rand((2, v), t, v, 3.0), **kw)
+
+
+def test_logits_long_histories():
+    """Histories of several rounds per block, crowded at a few ids, on one tile to many."""
+    for b, v, h, ids in ((1, 700, 5000, torch.int64), (3, 9000, 9001, torch.int32), (2, 70001, 3000, torch.int64),
+                         (40, 4100, 1025, torch.int32)):
+        kw = options(b, v, h, 3, v, ids)
+        kw["tokens"][:, ::3] = 1
+        kw["lens"][0] = h
+        kw.pop("mask")
+        check_logits(rand((b, v), BF, v, 3.0), **kw)
+
+
 def test_logits_duplicate_biases_add_in_order():
     z = torch.zeros(1, 64, device="cuda")
     ids = torch.tensor([[5] * 40 + [6, 5, 6]], device="cuda")
