@@ -9,8 +9,8 @@ namespace flce {
 namespace {
 
 // dw[j] = sum over blocks of part[b][j], in a fixed order: 32 columns per
-// block, warp k takes the partial rows k, k + 16, ...
-constexpr int kReduceWarps = 16;
+// block, warp k takes the partial rows k, k + 32, ...
+constexpr int kReduceWarps = 32;
 __global__ void __launch_bounds__(kReduceWarps * 32) dweight_reduce_kernel(const float* part, int blocks, int cols,
                                                                            void* dw, int dtype) {
   __shared__ float s[kReduceWarps][32];
@@ -108,7 +108,7 @@ int forward(const flce_norm_problem* p, const void* x, const void* residual, con
   DeviceInfo dev;
   FLCE_TRY(get_device(&dev));
   FLCE_TRY(check_local(dev, x, residual, weight, h, y, rstd, scale));
-  Phases ph{int(16 / es)};
+  Phases ph{vec_of(es, er)};
   ph.add(x, p->x_stride, p->rows, es);
   ph.add(residual, p->residual_stride, p->rows, er);
   ph.add(h, p->h_stride, p->rows, er);
@@ -211,7 +211,7 @@ int flce_add_rms_norm_backward(const flce_norm_problem* problem, const void* dy,
   n.offset = p->weight_offset;
   int blocks = 0;
   if (p->rows > 0) {
-    Phases ph{int(16 / es)};
+    Phases ph{vec_of(es, er)};
     ph.add(dy, n.dys, n.rows, es);
     ph.add(h, n.hs, n.rows, er);
     ph.add(dh, n.dhs, n.rows, er);

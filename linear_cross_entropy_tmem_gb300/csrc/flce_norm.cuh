@@ -36,6 +36,14 @@ constexpr int kMaxThreads = 1024;
 constexpr int kLoopThreads = 1024;    // rows too wide for registers
 constexpr float kE4m3Max = 448.0f;
 
+// Elements of a vector: 16 bytes of the wider of the call's two types, so that
+// neighbouring threads' accesses leave no gaps.  (With 8 elements for a 16-bit x
+// and an fp32 residual, 32 bytes per thread in two accesses, half of every sector
+// asked for was unused.)
+inline int vec_of(size_t elem, size_t residual_elem) { return int(16 / std::max(elem, residual_elem)); }
+template <class T, class R>
+constexpr int kVecOf = 16 / (sizeof(T) > sizeof(R) ? sizeof(T) : sizeof(R));
+
 // How a row is laid over threads, 16 elements per thread at most.
 enum RowForm {
   kWarp,    // a warp per row, kWarpRowBlock threads
@@ -128,8 +136,15 @@ __device__ __forceinline__ float pair_sum(uint64_t p) {
   return lo + hi;
 }
 
-__device__ __forceinline__ void cp_async16(void* dst_smem, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst_smem)), "l"(src) : "memory");
+template <int kBytes>
+__device__ __forceinline__ void cp_async(void* dst_smem, const void* src) {
+  if constexpr (kBytes == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst_smem)), "l"(src) : "memory");
+  } else {
+    static_assert(kBytes == 8 || kBytes == 4, "cp.async takes 4, 8 or 16 bytes");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst_smem)), "l"(src), "n"(kBytes)
+                 : "memory");
+  }
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits for all but the last n committed groups of this thread.
@@ -150,6 +165,11 @@ struct RowVectors {
     return kRagged ? col(i) + k >= 0 && col(i) + k < cols : col(i) < cols;
   }
 
+  // What is copied at once of a vector of type E: 16 bytes, or less.
+  template <class E>
+  static __host__ __device__ constexpr int word_of() {
+    return V * sizeof(E) < 16 ? int(V * sizeof(E)) : 16;
+  }
   // Bytes of one row's vectors of type E, all threads'.
   template <class E>
   __device__ __forceinline__ int bytes() const { return NV * width * int(sizeof(E)); }
@@ -157,24 +177,28 @@ struct RowVectors {
   // Starts copying the thread's whole vectors of a row into its slots.
   template <class E>
   __device__ __forceinline__ void fetch(const E* row, uint8_t* slots) const {
-    constexpr int kWords = V * sizeof(E) / 16;
+    if constexpr (V > 1) {
+      constexpr int kWord = word_of<E>(), kWords = V * sizeof(E) / kWord;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (whole(i))
+      for (int i = 0; i < NV; ++i)
+        if (whole(i))
 #pragma unroll
-        for (int c = 0; c < kWords; ++c)
-          cp_async16(slot(slots, i * kWords + c), reinterpret_cast<const uint8_t*>(row + col(i)) + c * 16);
+          for (int c = 0; c < kWords; ++c)
+            cp_async<kWord>(slot<kWord>(slots, i * kWords + c),
+                            reinterpret_cast<const uint8_t*>(row + col(i)) + c * kWord);
+    }
   }
   // The vectors that fetch() brought, once its copies have arrived; of the
   // others, a row's ragged ends, `edge` holds the elements.
   template <class E>
   __device__ __forceinline__ Vec<E, V> read(uint8_t* slots, int i, const Vec<E, V> (&edge)[NV]) const {
     if (!whole(i)) return edge[i];
-    constexpr int kWords = V * sizeof(E) / 16;
+    constexpr int kWord = word_of<E>(), kWords = V * sizeof(E) / kWord;
+    using Word = Vec<uint32_t, kWord / 4>;
     Vec<E, V> x;
 #pragma unroll
     for (int c = 0; c < kWords; ++c)
-      reinterpret_cast<uint4*>(&x)[c] = *reinterpret_cast<const uint4*>(slot(slots, i * kWords + c));
+      reinterpret_cast<Word*>(&x)[c] = *reinterpret_cast<const Word*>(slot<kWord>(slots, i * kWords + c));
     return x;
   }
   // A row's ragged ends, by element; 0 outside the row.
@@ -204,8 +228,9 @@ struct RowVectors {
         if (has(i, k)) row[col(i) + k] = x.v[k];
     }
   }
+  template <int kWord>
   __device__ __forceinline__ uint8_t* slot(uint8_t* slots, int word) const {
-    return slots + (word * (width / V) + thread) * 16;
+    return slots + (word * (width / V) + thread) * kWord;
   }
   // The thread's weights, offset added, into its slots of a region of
   // bytes<float>(); then vector i's.
@@ -221,7 +246,7 @@ struct RowVectors {
   }
   __device__ __forceinline__ float* weight_at(uint8_t* slots, int i, int k) const {
     if constexpr (V == 1) return reinterpret_cast<float*>(slots) + i * width + thread;
-    return reinterpret_cast<float*>(slot(slots, i * (V / 4) + k / 4)) + k % 4;
+    return reinterpret_cast<float*>(slot<16>(slots, i * (V / 4) + k / 4)) + k % 4;
   }
   __device__ __forceinline__ Floats<V> weight(uint8_t* slots, int i) const {
     Vec<float, V> x;
@@ -230,7 +255,7 @@ struct RowVectors {
     } else {
 #pragma unroll
       for (int c = 0; c < V / 4; ++c)
-        reinterpret_cast<uint4*>(&x)[c] = *reinterpret_cast<const uint4*>(slot(slots, i * (V / 4) + c));
+        reinterpret_cast<uint4*>(&x)[c] = *reinterpret_cast<const uint4*>(slot<16>(slots, i * (V / 4) + c));
     }
     return widen(x);
   }

@@ -218,7 +218,7 @@ cudaError_t launch_bwd(const NormBwdParams& p, const RowPlan& pl, int blocks, cu
 template <class T, class R>
 cudaError_t launch_bwd_types(const NormBwdParams& p, const RowPlan& pl, int blocks, cudaStream_t st) {
   if (pl.vec == 1) return launch_bwd<T, R, 1>(p, pl, blocks, st);
-  return launch_bwd<T, R, 16 / sizeof(T)>(p, pl, blocks, st);
+  return launch_bwd<T, R, kVecOf<T, R>>(p, pl, blocks, st);
 }
 
 }  // namespace

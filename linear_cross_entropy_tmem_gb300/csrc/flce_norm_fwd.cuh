@@ -229,20 +229,20 @@ __global__ void __launch_bounds__(kLoopThreads) norm_fwd_loop_kernel(NormParams 
     load_weight<1>(p.w, p.w_dtype, p.offset, c, w);
     return (p.r ? to_f32(h[c]) : to_f32(x[c])) * rstd * w[0];
   };
-  if (!kFp8) {
+  if constexpr (!kFp8) {
     T* y = static_cast<T*>(p.y) + row * p.ys;
     for (int c = threadIdx.x; c < p.cols; c += kLoopThreads) y[c] = from_f32<T>(value(c));
-    return;
+  } else {
+    for (int g = threadIdx.x; g < p.groups; g += kLoopThreads) amax[g] = 0u;
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.cols; c += kLoopThreads) atomicMax(&amax[c / p.group], abs_bits(value(c)));
+    __syncthreads();
+    for (int g = threadIdx.x; g < p.groups; g += kLoopThreads)
+      p.scale[row * p.groups + g] = scale_of(amax[g]);
+    uint8_t* q = static_cast<uint8_t*>(p.y) + row * p.ys;
+    for (int c = threadIdx.x; c < p.cols; c += kLoopThreads)
+      q[c] = quantise(value(c), inverse_of(scale_of(amax[c / p.group])));
   }
-  for (int g = threadIdx.x; g < p.groups; g += kLoopThreads) amax[g] = 0u;
-  __syncthreads();
-  for (int c = threadIdx.x; c < p.cols; c += kLoopThreads) atomicMax(&amax[c / p.group], abs_bits(value(c)));
-  __syncthreads();
-  for (int g = threadIdx.x; g < p.groups; g += kLoopThreads)
-    p.scale[row * p.groups + g] = scale_of(amax[g]);
-  uint8_t* q = static_cast<uint8_t*>(p.y) + row * p.ys;
-  for (int c = threadIdx.x; c < p.cols; c += kLoopThreads)
-    q[c] = quantise(value(c), inverse_of(scale_of(amax[c / p.group])));
 }
 
 template <class T, class R, int V, bool kFp8>
@@ -270,7 +270,7 @@ cudaError_t launch_fwd(const NormParams& p, const RowPlan& pl, int grid, cudaStr
 template <class T, class R, bool kFp8>
 cudaError_t launch_fwd_types(const NormParams& p, const RowPlan& pl, int grid, cudaStream_t st) {
   if (pl.vec == 1) return launch_fwd<T, R, 1, kFp8>(p, pl, grid, st);
-  return launch_fwd<T, R, 16 / sizeof(T), kFp8>(p, pl, grid, st);
+  return launch_fwd<T, R, kVecOf<T, R>, kFp8>(p, pl, grid, st);
 }
 
 template <bool kFp8>
