@@ -32,6 +32,7 @@ constexpr int64_t kWantChunks = 8000; // so that there are about this many at mo
 constexpr int kMaxGrid = 32768;       // blocks of a launch at most: partial sums per launch
 constexpr int kFewParts = 512;       // up to here every block of the second pass adds the partial sums itself
 constexpr int kSmallTable = 32;       // tensors per launch: the small table is copied faster
+constexpr int kMediumTable = 240;
 constexpr int kLargeTable = 960;      // (27.9 KB of the 32 KB of kernel parameters)
 
 // One launch's tensors: chunk_end[i] is the number of chunks of tensors 0..i.
@@ -379,8 +380,9 @@ int run(const Grads& g, bool clip, float max_norm, float* norm, void* workspace,
   }
   double* part = static_cast<double*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return g.count <= kSmallTable ? run_tables<kSmallTable>(g, clip, max_norm, norm, part, st)
-                                : run_tables<kLargeTable>(g, clip, max_norm, norm, part, st);
+  if (g.count <= kSmallTable) return run_tables<kSmallTable>(g, clip, max_norm, norm, part, st);
+  if (g.count <= kMediumTable) return run_tables<kMediumTable>(g, clip, max_norm, norm, part, st);
+  return run_tables<kLargeTable>(g, clip, max_norm, norm, part, st);
 }
 
 }  // namespace

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(row_threads(kForm), fwd_blocks(kForm, kRagged)
     }
     const float ss = kWarpRow ? warp_sum(pair_sum(squares)) : block_sum(pair_sum(squares), red[turn]);
     turn ^= 1;
-    const float rstd = 1.0f / sqrtf(ss / float(p.cols) + p.eps);
+    const float rstd = rsqrtf(ss * (1.0f / float(p.cols)) + p.eps);
     if (t == 0 && p.rstd) p.rstd[row] = rstd;
     const uint64_t rstd2 = f2_splat(rstd);
 #pragma unroll
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kLoopThreads) norm_fwd_loop_kernel(NormParams 
     ss = fmaf(f, f, ss);
   }
   ss = block_sum(ss, red);
-  const float rstd = 1.0f / sqrtf(ss / float(p.cols) + p.eps);
+  const float rstd = rsqrtf(ss * (1.0f / float(p.cols)) + p.eps);
   if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
   auto value = [&](int c) {
     float w[1];
