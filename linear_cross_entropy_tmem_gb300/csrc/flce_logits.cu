@@ -136,6 +136,7 @@ __device__ __forceinline__ int place(const Span& s, int32_t id) {
 // A list of ids read by the block, kIds of them per thread under way at once.
 constexpr int kIds = 8;
 constexpr int kIdsBlock = kIds * kRowThreads;
+constexpr int kBiases = 2;  // biases per thread that are read at the start
 struct Ids {
   const void* p;
   int i64;
@@ -266,8 +267,8 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
   span.count = max(0, min(span.first + kTile, p.vocab) - span.begin);  // 0: the row ends before the tile
   const int first = span.first;
 
-  // The loads of the lists and of the tile go out together.  The first ids are
-  // loaded whatever the row's length, which is under way too.
+  // The loads of the lists go out before the tile's.  The first ids are loaded
+  // whatever the row's length.
   const bool named = p.tokens || p.n_bias;
   const int history = p.tokens ? int(p.history) : 0;
   const Ids ids = {p.tokens_i64 ? static_cast<const void*>(static_cast<const int64_t*>(p.tokens) + row * p.ts)
@@ -278,7 +279,13 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
                             : static_cast<const void*>(static_cast<const int32_t*>(p.bias_ids) + row * p.bis),
                         p.bias_ids_i64};
   int ids_at[kIds];
-  int bias_at = -1;
+  int bias_at[kBiases];
+  if (history) ids.load(0, history, span, ids_at);
+#pragma unroll
+  for (int u = 0; u < kBiases; ++u) {
+    const int i = u * kRowThreads + int(threadIdx.x);
+    bias_at[u] = i < p.n_bias ? bias_ids.one(i, span) : -1;
+  }
   Vec<T, V> x[NV];   // as loaded: a conversion here would wait for its load before the next is issued
   uint32_t bits[NV];
   const bool inner = first >= 0 && first + kTile <= p.vocab;
@@ -327,8 +334,6 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
       }
     }
   }
-  if (history) ids.load(0, history, span, ids_at);
-  if (int(threadIdx.x) < p.n_bias) bias_at = bias_ids.one(threadIdx.x, span);
 
   if (named) {
     constexpr int kWords = kTile + 2 * (kTile / 32) + 4;  // up to the list
@@ -359,13 +364,15 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
         old[u] = count_id(&s.table[max(ids_at[u], 0)], ids_at[u] >= 0, base + u * kRowThreads + int(threadIdx.x) < prompt);
       append(s, ids_at, old);
     }
-    for (int i = threadIdx.x; i < p.n_bias; i += kRowThreads) {
-      const int at = i < kRowThreads ? bias_at : bias_ids.one(i, span);
+    auto name = [&](int at) {
       if (at >= 0) {
         s.biased = 1;
         if (!mark(s.seen, at)) s.twice = 1;
       }
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < kBiases; ++u) name(bias_at[u]);
+    for (int i = kBiases * kRowThreads + threadIdx.x; i < p.n_bias; i += kRowThreads) name(bias_ids.one(i, span));
     __syncthreads();
 
     // One thread per listed place works out its value from the logit (in L1:
@@ -398,7 +405,7 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
       };
       if (!s.twice) {
         for (int i = threadIdx.x; i < p.n_bias; i += kRowThreads) {
-          const int at = i < kRowThreads ? bias_at : bias_ids.one(i, span);
+          const int at = bias_ids.one(i, span);
           if (at >= 0) add(at, bias[i]);
         }
       } else {  // some entry has several: their sum, in the list's order, once
