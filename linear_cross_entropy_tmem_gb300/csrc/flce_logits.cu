@@ -280,6 +280,8 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
                         p.bias_ids_i64};
   int ids_at[kIds];
   int bias_at[kBiases];
+  const int64_t len64 = history && p.lens ? p.lens[row] : history;
+  const int64_t prompt64 = history && p.prompt_lens ? p.prompt_lens[row] : 0;
   if (history) ids.load(0, history, span, ids_at);
 #pragma unroll
   for (int u = 0; u < kBiases; ++u) {
@@ -339,8 +341,8 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
     constexpr int kWords = kTile + 2 * (kTile / 32) + 4;  // up to the list
     for (int i = threadIdx.x * 4; i < kWords; i += kRowThreads * 4)
       *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
-    const int len = p.lens ? int(min(max(p.lens[row], int64_t(0)), int64_t(history))) : history;
-    const int prompt = p.prompt_lens ? int(min(max(p.prompt_lens[row], int64_t(0)), int64_t(history))) : 0;
+    const int len = int(min(max(len64, int64_t(0)), int64_t(history)));
+    const int prompt = int(min(max(prompt64, int64_t(0)), int64_t(history)));
     const bool has_rep = p.repetition != nullptr;
     const float rep = has_rep ? p.repetition[row] : 1.f;
     const float pres = p.presence ? p.presence[row] : 0.f;
