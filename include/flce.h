@@ -409,8 +409,8 @@ typedef struct {
  *   residual [N, D] or NULL
  *   weight   [D] or NULL
  *   h        [N, D] written when there is a residual (may be the residual's own
- *            memory), NULL without one
- *   y        [N, D] (may be x's own memory)
+ *            memory, with its stride), NULL without one
+ *   y        [N, D] (may be x's own memory, with its stride)
  *   rstd     [N] fp32 for the backward, or NULL
  */
 FLCE_API int flce_add_rms_norm(const flce_norm_problem* problem, const void* x, const void* residual,
@@ -438,7 +438,7 @@ FLCE_API int flce_add_rms_norm_workspace_size(const flce_norm_problem* problem, 
  *   dweight_j = sum over rows of dy_j n_j, in weight_dtype (NULL: not formed)
  *   dy  [N, D] gradient of y;  dh [N, D] gradient of h from its other uses
  *   h, rstd: of the forward (h is x when there was no residual)
- *   dx may be dy's own memory, and dresidual dh's.
+ *   dx may be dy's own memory, and dresidual dh's, with the same strides.
  */
 FLCE_API int flce_add_rms_norm_backward(const flce_norm_problem* problem, const void* dy, const void* h,
                                         const void* weight, const float* rstd, const void* dh, void* dx,
@@ -468,7 +468,8 @@ FLCE_API int flce_grad_norm(const void* const* grads, const int64_t* numel, cons
  * gives NaN gradients; an infinite one c = 0.
  *   outs    host array of device pointers: where each clipped gradient goes,
  *           its own memory (in place) or a dense tensor of the same type that
- *           overlaps no gradient.  In place, nothing is written when c is 1.
+ *           overlaps no gradient and no other out.  In place, nothing is written
+ *           when c is 1, and no two gradients may overlap (a tensor listed twice).
  *   max_norm  >= 0, not NaN (infinity leaves the gradients as they are)
  */
 FLCE_API int flce_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numel,
@@ -516,7 +517,8 @@ FLCE_API int flce_process_logits_workspace_size(const flce_logits_problem* probl
  *   bias_ids [B, K] ids and bias [B, K] fp32, both or neither; ids outside
  *            [0, V) are padding
  *   mask     [B, ceil(V / 32)] 32-bit words, or NULL
- *   out      [B, V] (may be the logits' own memory when the types are the same)
+ *   out      [B, V] (may be the logits' own memory, with its stride, when the types
+ *            are the same)
  *   token    [B] int64 or NULL;  lse [B] fp32 or NULL
  */
 FLCE_API int flce_process_logits(const flce_logits_problem* problem, const void* logits, const void* tokens,

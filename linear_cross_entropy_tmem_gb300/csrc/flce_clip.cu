@@ -3,8 +3,10 @@
 //
 //   norm = sqrt(sum g^2),  c = min(1, max_norm / (norm + 1e-6)),  out = rn(g c)
 //
-// Two passes over the gradients, both bound by memory (the second may find the
-// end of what the first read in L2, so it goes backwards).  The tensors' pointers
+// Two passes over the gradients, both bound by memory: 622 M bf16 elements of a
+// head's gradients take 560 us, where reading twice and writing once at the copy
+// rate takes 557.  The second pass may find the end of what the first read in L2, so it goes
+// backwards.  The tensors' pointers
 // and sizes travel in the kernels' parameters (no copy to the device, nothing
 // for the caller to keep), and the tensors of a type are cut into chunks of one
 // size, a block each, so that many small tensors cost no more than a few large
@@ -12,7 +14,7 @@
 //
 // fp64 is slow on this part (two lanes per SM and clock): with an fp64 addition
 // per 32 elements and fp64 sums over the block the first pass ran at half the
-// memory's rate.  So a chunk is summed in fp32, compensated over its rounds, and
+// memory's rate (head: 1021 us; 34 M fp32 elements: 95, now 72).  So a chunk is summed in fp32, compensated over its rounds, and
 // only chunks whose squares leave fp32's safe range are summed again in fp64.
 #include <algorithm>
 #include <cmath>
@@ -30,7 +32,7 @@ constexpr int kUnroll = 4;            // 16-byte loads under way per thread
 constexpr int kMinChunk = 8192;       // elements per chunk: this times a power of two,
 constexpr int64_t kWantChunks = 8000; // so that there are about this many at most
 constexpr int kMaxGrid = 32768;       // blocks of a launch at most: partial sums per launch
-constexpr int kFewParts = 512;       // up to here every block of the second pass adds the partial sums itself
+constexpr int kFewParts = 512;        // up to here every block of the second pass adds the partial sums itself
 constexpr int kSmallTable = 32;       // tensors per launch: the small table is copied faster
 constexpr int kMediumTable = 240;
 constexpr int kLargeTable = 960;      // (27.9 KB of the 32 KB of kernel parameters)
@@ -151,6 +153,9 @@ __device__ __forceinline__ double block_tree(double x, double* red) {
   return red[0];
 }
 
+// The first pass: each block adds up chunks and writes one partial sum.  kUnroll
+// loads per thread under way and blocks of one chunk keep it at the copy rate;
+// with chunks of about 8000 per call the partial sums stay few.
 template <int N, class T>
 __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_constant__ GradTable<N> t, double* part) {
   __shared__ double red[kGradThreads];
@@ -187,6 +192,9 @@ __device__ __forceinline__ double total(const double* part, int n, double* red) 
   return block_tree(s, red);
 }
 
+// The partial sums' total where there are many, or where nothing is clipped: one
+// block, in fp64 and in a fixed order.  It is latency: about 5 us behind 8000
+// partial sums (34 M fp32 elements), 1 % of the head's two passes.
 __global__ void __launch_bounds__(kTotalThreads) norm_total_kernel(const double* part, int n, float* norm) {
   __shared__ double red[kTotalThreads];
   griddep_release();
@@ -245,6 +253,9 @@ __device__ __forceinline__ float clip_factor(float norm, float max_norm) {
   return c > 1.0f ? 1.0f : c;
 }
 
+// The second pass.  Up to kFewParts partial sums every block adds up itself
+// rather than wait for one more launch: 112 tensors of adapters (3.7 M bf16 elements)
+// take 11.7 us for both passes.
 template <int N, class T>
 __global__ void __launch_bounds__(kGradThreads, 4) grad_scale_kernel(const __grid_constant__ GradTable<N> t,
                                                              const double* part, int n_part, float max_norm,

@@ -36,23 +36,12 @@ __device__ __forceinline__ Vec<T, V> load_vec(const T* p) { return *reinterpret_
 template <class T, int V>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& x) { *reinterpret_cast<Vec<T, V>*>(p) = x; }
 
-template <int V>
-__device__ __forceinline__ void load_as_f32(const void* p, int dtype, int64_t i, float (&out)[V]) {
-  if (dtype == FLCE_F32) {
-    const Vec<float, V> x = load_vec<float, V>(static_cast<const float*>(p) + i);
-#pragma unroll
-    for (int k = 0; k < V; ++k) out[k] = x.v[k];
-  } else if (dtype == FLCE_BF16) {
-    const Vec<__nv_bfloat16, V> x = load_vec<__nv_bfloat16, V>(static_cast<const __nv_bfloat16*>(p) + i);
-#pragma unroll
-    for (int k = 0; k < V; ++k) out[k] = to_f32(x.v[k]);
-  } else {
-    const Vec<__half, V> x = load_vec<__half, V>(static_cast<const __half*>(p) + i);
-#pragma unroll
-    for (int k = 0; k < V; ++k) out[k] = to_f32(x.v[k]);
-  }
+// One element of a type known at run time.
+__device__ __forceinline__ float load_as(const void* p, int dtype, int64_t i) {
+  if (dtype == FLCE_F32) return static_cast<const float*>(p)[i];
+  if (dtype == FLCE_BF16) return to_f32(static_cast<const __nv_bfloat16*>(p)[i]);
+  return to_f32(static_cast<const __half*>(p)[i]);
 }
-
 __device__ __forceinline__ void store_as(void* p, int dtype, int64_t i, float x) {
   if (dtype == FLCE_F32) {
     static_cast<float*>(p)[i] = x;
@@ -63,27 +52,20 @@ __device__ __forceinline__ void store_as(void* p, int dtype, int64_t i, float x)
   }
 }
 
-// Sums over a warp (every lane gets the same value, in a fixed order).
+// Sum over a warp (every lane gets the same value, in a fixed order).
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-__device__ __forceinline__ double warp_sum(double x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
 // Sum over the block (every thread gets it); `buf` holds 32 values, and the
 // call after next may reuse it (callers in a loop alternate two buffers).
-template <class F>
-__device__ __forceinline__ F block_sum(F x, F* buf) {
+__device__ __forceinline__ float block_sum(float x, float* buf) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = (blockDim.x + 31) >> 5;
   x = warp_sum(x);
   if (lane == 0) buf[warp] = x;
   __syncthreads();
-  return warp_sum(lane < warps ? buf[lane] : F(0));
+  return warp_sum(lane < warps ? buf[lane] : 0.f);
 }
 
 // As a programmatic dependent of the kernel before it on the stream (it

@@ -15,6 +15,15 @@
 // and marks it in a bitmap.  The dense pass only looks at the bitmap: a test per
 // vector instead of a table look-up and a division's code per entry.  Rounding,
 // maximum and sum come from registers, the maximum before the first exponential.
+//
+// 256 x 262144 fp32 to fp32: 81 us without a history, what the copy rate gives;
+// 129 us with histories of up to 2048, 300 biases and a mask.  Each of a row's
+// blocks scans the whole history for its own tile, and that scan with its
+// shared-memory atomics and barriers is what keeps the blocks from their loads.
+// Smaller tiles scan more often, larger ones leave fewer blocks to overlap:
+// 16 entries per thread 168 us, 512 threads 171, a history shared by a cluster
+// of 8 blocks 199, a kernel of its own for the named entries 124 (but 12 us in
+// place of 8 for a single row, and 37 us in place of 23 for 64).
 #include <algorithm>
 #include <cmath>
 
@@ -245,6 +254,7 @@ __device__ __forceinline__ void append(Named<kTile>& s, const int (&at)[kIds], c
     if (old[u] == 0) s.list[pos++] = uint16_t(at[u]);
 }
 
+// 1 x 151936 fp32 with everything: 8 us, of which a launch and its merge are 4.
 // A block's tile is kRowThreads * V * NV entries; thread t holds the vectors at
 // (t + i * kRowThreads) * V.  Vectors are aligned in memory: a row whose first
 // element is `shift` elements past a 16-byte boundary starts `shift` entries
@@ -508,7 +518,8 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
 }
 
 // One warp per row joins the tiles' statistics, and finds the first entry of
-// the vector of `vec` that holds the maximum.
+// the vector of `vec` that holds the maximum.  Set up while the tiles' kernel
+// runs: it adds 1.5 us or so of latency and no traffic to speak of.
 template <class O>
 __global__ void __launch_bounds__(kRowThreads) merge_logits_kernel(const Partial* part, int64_t rows, int tiles,
                                                                   const O* out, int64_t os, int vocab, int vec,

@@ -165,7 +165,9 @@ int flce_add_rms_norm_fp8(const flce_norm_problem* problem, const void* x, const
 int flce_add_rms_norm_workspace_size(const flce_norm_problem* problem, size_t* bytes) {
   if (!bytes) return FLCE_ERR_INVALID_ARG;
   FLCE_TRY(validate(problem));
-  *bytes = size_t(std::min<int64_t>(problem->rows, kMaxBwdBlocks)) * size_t(problem->cols) * 4 + 256;
+  // a partial dweight row per block; rows over 16 elements x 1024 threads take kLoopSplits
+  const int64_t blocks = problem->cols > 16 * kMaxThreads ? kLoopSplits : kMaxBwdBlocks;
+  *bytes = size_t(std::min<int64_t>(problem->rows, blocks)) * size_t(problem->cols) * 4 + 256;
   return FLCE_OK;
 }
 
@@ -218,10 +220,10 @@ int flce_add_rms_norm_backward(const flce_norm_problem* problem, const void* dy,
     ph.add(dx, n.dxs, n.rows, es);
     ph.add(dresidual, n.drs, n.rows, er);
     const RowPlan pl = ph.plan(n.cols);
-      blocks = pl.form == kLoop ? int(std::min<int64_t>(n.rows, kLoopSplits))
-                : std::min(kMaxBwdBlocks, row_blocks(pl, n.rows, dev.num_sms,
-                                                               bwd_blocks(pl.form, pl.ragged, pl.vec * pl.nv),
-                                                               row_smem(pl, es + 2 * er), 1));
+    blocks = pl.form == kLoop
+                 ? int(std::min<int64_t>(n.rows, kLoopSplits))
+                 : std::min(kMaxBwdBlocks, row_blocks(pl, n.rows, dev.num_sms, bwd_blocks(pl.form, pl.ragged, pl.vec * pl.nv),
+                                                      row_smem(pl, es + 2 * er), 1));
     FLCE_TRY(logged(FLCE_LAUNCH_OTHER, st,
                     [&] { return launch_norm_bwd(n, p->dtype, p->residual_dtype, pl, blocks, st); }));
   }

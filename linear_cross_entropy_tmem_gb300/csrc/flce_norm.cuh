@@ -10,16 +10,18 @@
 // row is read once and stays in registers between its reduction and its output.
 // The rows after it are already being copied into shared memory, each thread's
 // own vectors into its own slots (cp.async), so that the bytes under way cost no
-// registers and need no barrier.  With that the issue slots are the next limit
-// (they were two thirds busy with 31 instructions per element), so the
-// arithmetic runs on pairs of fp32 lanes, and the weights wait in shared memory
-// as fp32 with their offset added.
+// registers and need no barrier (next row in registers instead: 217 us, for too
+// few threads fit; three rows ahead: no faster than two).  With that the issue
+// slots are the next limit (two thirds busy in the forward), so the arithmetic runs on
+// pairs of fp32 lanes (backward 118 -> 94 us), and the weights wait in shared
+// memory as fp32 with their offset added.  (Times: 16384 x 4096 bf16.)
 //
 // Rows need not start on 16-byte boundaries.  A row whose first element is
 // `shift` elements past one is laid over threads `shift` places late, so that
-// all its vectors but the first and the last are 16 aligned bytes.  A block (or
-// warp) takes rows a multiple of the vector's width apart, which all have the
-// same shift: its columns, weights and dweight sums stay in its registers.
+// all its vectors but the first and the last are 16 aligned bytes (4099 x 1283
+// bf16 with an fp32 residual, backward: 22 us; as single elements 74).  A block (or warp) takes rows a
+// multiple of the vector's width apart, which all have the same shift: a thread's
+// columns, its weights and its dweight sums are the same for all its rows.
 #pragma once
 
 #include <algorithm>
@@ -83,16 +85,9 @@ struct NormParams {
   float eps, offset;
 };
 
-template <int V>
-__device__ __forceinline__ void load_weight(const void* w, int dtype, float offset, int col, float (&out)[V]) {
-  if (w) {
-    load_as_f32<V>(w, dtype, col, out);
-  } else {
-#pragma unroll
-    for (int k = 0; k < V; ++k) out[k] = 1.0f;
-  }
-#pragma unroll
-  for (int k = 0; k < V; ++k) out[k] += offset;
+// w_j + o; without weights 1 + o.
+__device__ __forceinline__ float load_weight(const void* w, int dtype, float offset, int col) {
+  return (w ? load_as(w, dtype, col) : 1.0f) + offset;
 }
 
 // V values in fp32, in pairs (V = 1: the other lane is 0).
@@ -238,11 +233,8 @@ struct RowVectors {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        float one[1] = {0.f};
-        if (has(i, k)) load_weight<1>(w, dtype, offset, col(i) + k, one);
-        *weight_at(slots, i, k) = one[0];
-      }
+      for (int k = 0; k < V; ++k)
+        *weight_at(slots, i, k) = has(i, k) ? load_weight(w, dtype, offset, col(i) + k) : 0.f;
   }
   __device__ __forceinline__ float* weight_at(uint8_t* slots, int i, int k) const {
     if constexpr (V == 1) return reinterpret_cast<float*>(slots) + i * width + thread;

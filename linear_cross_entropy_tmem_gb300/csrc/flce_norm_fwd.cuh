@@ -39,7 +39,13 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
 // one gets a NaN scale.
 __device__ __forceinline__ uint32_t abs_bits(float y) { return __float_as_uint(y) & 0x7fffffffu; }
 
-// Rows go to warps (kWarpRow) or to blocks, in turn.
+// Rows go to warps (kWarpRow) or to blocks, in turn.  h is rounded to its type
+// before its squares are summed, as the backward reads it rounded.
+// 16384 x 4096 bf16 with residual: 81.6 us, 6.6 TB/s, what a copy reaches; one
+// row of 4096: 3.4 us, a launch.  With the 8-bit output and groups of 128, 8192 x
+// 2048 fp16 takes 28 us for 118 MB (4.2 TB/s): groups' maxima, the division by
+// the scale and the conversion bring it to about 35 instructions per element, and
+// issue slots are the bound.
 template <class T, class R, int V, int NV, RowForm kForm, bool kRagged, bool kFp8>
 __global__ void __launch_bounds__(row_threads(kForm), fwd_blocks(kForm, kRagged)) norm_fwd_kernel(NormParams p) {
   constexpr bool kWarpRow = kForm == kWarp;
@@ -201,8 +207,9 @@ __global__ void __launch_bounds__(row_threads(kForm), fwd_blocks(kForm, kRagged)
   }
 }
 
-// Rows too wide for registers: one block per row, which reads h (its own
-// writes: each thread returns to the columns it wrote) once more per pass.
+// Rows too wide for registers (over 16384 columns): one block per row, which
+// reads h (its own writes: each thread returns to the columns it wrote) once more
+// per pass, from L2 as a rule.
 template <class T, class R, bool kFp8>
 __global__ void __launch_bounds__(kLoopThreads) norm_fwd_loop_kernel(NormParams p) {
   extern __shared__ uint32_t amax[];
@@ -225,9 +232,7 @@ __global__ void __launch_bounds__(kLoopThreads) norm_fwd_loop_kernel(NormParams 
   const float rstd = rsqrtf(ss * (1.0f / float(p.cols)) + p.eps);
   if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
   auto value = [&](int c) {
-    float w[1];
-    load_weight<1>(p.w, p.w_dtype, p.offset, c, w);
-    return (p.r ? to_f32(h[c]) : to_f32(x[c])) * rstd * w[0];
+    return (p.r ? to_f32(h[c]) : to_f32(x[c])) * rstd * load_weight(p.w, p.w_dtype, p.offset, c);
   };
   if constexpr (!kFp8) {
     T* y = static_cast<T*>(p.y) + row * p.ys;

@@ -175,8 +175,8 @@ def flce_add_rms_norm_fp8(x: torch.Tensor, weight: Optional[torch.Tensor] = None
                           group: int = 128) -> AddRmsNormFp8Result:
     """The forward with an e4m3 output and one fp32 scale per ``group`` columns of a row (0: per row; see
     ``flce_add_rms_norm_fp8``)."""
-    if group < 0:
-        raise ValueError(f"flce: group must not be negative, got {group}")
+    if not 0 <= group <= 1 << 20:
+        raise ValueError(f"flce: group must be 0 or a multiple of 16, got {group}")
     out = _call("add_rms_norm", x, weight, residual, eps, weight_offset, False, int(group))
     q, h, s = out if out is not None else _norm_forward(x, weight, residual, eps, weight_offset, rstd=False,
                                                         group=int(group))
@@ -349,7 +349,8 @@ def clip_grad_norm_(grads: Iterable[torch.Tensor], max_norm: float, *,
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Scale ``grads`` by min(1, max_norm / (norm + 1e-6)) in place, or into ``outputs`` (tensors of the same
     dtypes and layouts, such as slices of an optimizer's flat buffer), and return the norm before clipping as a
-    0-dim fp32 device tensor (see ``flce_clip_grad_norm``).  Nothing waits for the device."""
+    0-dim fp32 device tensor (see ``flce_clip_grad_norm``).  Nothing waits for the device.  List no gradient twice,
+    and none that overlaps another: they are scaled side by side."""
     grads = list(grads)
     outputs = None if outputs is None else list(outputs)
     max_norm = float(max_norm)
