@@ -16,14 +16,15 @@
 // vector instead of a table look-up and a division's code per entry.  Rounding,
 // maximum and sum come from registers, the maximum before the first exponential.
 //
-// 256 x 262144 fp32 to fp32: 81 us without a history, what the copy rate gives;
-// 129 us with histories of up to 2048, 300 biases and a mask.  Each of a row's
-// blocks scans the whole history for its own tile, and that scan with its
-// shared-memory atomics and barriers is what keeps the blocks from their loads.
+// 256 x 262144 fp32 to fp32: 81 us without options, what the copy rate gives;
+// 98 us with a mask and 300 biases, 126 us with histories of up to 2048 as well.
+// Each of a row's blocks scans the whole history for its own tile, and that scan
+// with its atomics and barriers is what keeps the blocks from their loads.
 // Smaller tiles scan more often, larger ones leave fewer blocks to overlap:
-// 16 entries per thread 168 us, 512 threads 171, a history shared by a cluster
-// of 8 blocks 199, a kernel of its own for the named entries 124 (but 12 us in
-// place of 8 for a single row, and 37 us in place of 23 for 64).
+// 128 threads 142 us, 16 entries per thread 168, 512 threads 171, four blocks on
+// an SM (registers spill) 161, the next ids loaded ahead (they do as well) 142, a
+// history shared by a cluster of 8 blocks 199, a kernel of its own for the named
+// entries 124 (but 12 us in place of 8 for a single row, 37 in place of 23 for 64).
 #include <algorithm>
 #include <cmath>
 
@@ -39,10 +40,6 @@ constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxPerThread = 32;       // entries a thread holds, at most: a tile of 8192
 constexpr int kMaxSingles = 16;         // the same without vectors (a mask word per entry takes registers)
 constexpr int64_t kWantBlocks = 456;    // three blocks on each of 152 SMs
-// A word of the table: how often an entry was answered, and whether the prompt
-// has it; later the entry's new value.
-constexpr uint32_t kPromptBit = 0x80000000u;
-constexpr uint32_t kCountMask = kPromptBit - 1;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int64_t kMaxIds = (int64_t(1) << 30) - 1;  // of a row's history, and of its biases
 
@@ -185,10 +182,9 @@ __device__ __forceinline__ float bias_sum(const Ids& ids, const float* bias, int
   return sum;
 }
 
-// Steps 1 and 2 of the chain for an entry of the history.
-__device__ __forceinline__ float penalise(float z, uint32_t word, float rep, float pres, float freq, bool has_rep) {
+// Steps 1 and 2 of the chain for an entry of the history, answered n times.
+__device__ __forceinline__ float penalise(float z, uint32_t n, float rep, float pres, float freq, bool has_rep) {
   if (has_rep) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-  const uint32_t n = word & kCountMask;
   if (n) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, float(n))), pres);
   return z;
 }
@@ -204,54 +200,29 @@ __device__ __forceinline__ bool mark(uint32_t* map, int at) {
 // What the row's history and biases say of a tile, in shared memory.
 template <int kTile>
 struct Named {
-  uint32_t table[kTile];      // counts, then new values at the marked places
-  uint32_t map[kTile / 32];   // marks
+  uint32_t table[kTile];      // how often an entry was answered; then, at the marked places, new values
+  uint32_t map[kTile / 32];   // marks: places of the history, then of the biases too
   uint32_t seen[kTile / 32];  // places that a bias names
-  int n_list;                 // entries of the list
   int biased, twice;          // whether a bias names a place, or one twice
-  int pad;
-  uint16_t list[kTile];       // the places that the history names, each once
+  int pad[2];
+  uint16_t list[kTile];       // the places that the history names, a part for each warp
 };
 
-// Counts one id if `in`: the prompt's mark, or one more answer.  Returns the
-// word before (1 if not `in`).  Predicated rather than branched to, so that a
-// thread's kIds atomics are under way together.
-__device__ __forceinline__ uint32_t count_id(uint32_t* word, bool in, bool prompt) {
-  uint32_t old = 1u;
+// Counts the id at place `at` (-1: none): its mark, and if it was answered its
+// count.  Predicated rather than branched to, and nothing comes back, so nothing
+// waits.
+template <int kTile>
+__device__ __forceinline__ void count_id(Named<kTile>& s, int at, bool answered) {
+  const int to = max(at, 0);
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %2, 0;\n\t"
-      "setp.ne.u32 q, %3, 0;\n\t"
-      "@p atom.shared.or.b32 %0, [%1], %4;\n\t"
-      "@q atom.shared.add.u32 %0, [%1], 1;\n\t}\n"
-      : "+r"(old)
-      : "r"(smem_u32(word)), "r"(uint32_t(in && prompt)), "r"(uint32_t(in && !prompt)), "r"(kPromptBit)
+      "setp.ge.s32 p, %2, 0;\n\t"
+      "setp.ne.and.u32 q, %3, 0, p;\n\t"
+      "@p red.shared.or.b32 [%0], %4;\n\t"
+      "@q red.shared.add.u32 [%1], 1;\n\t}"
+      ::"r"(smem_u32(&s.map[to >> 5])), "r"(smem_u32(&s.table[to])), "r"(at), "r"(uint32_t(answered)),
+      "r"(1u << (to & 31))
       : "memory");
-  return old;
-}
-
-// Whoever met a place first (the word before was 0) puts it on the list; whole
-// warps, one addition to the list's length for all of a warp's places.
-template <int kTile>
-__device__ __forceinline__ void append(Named<kTile>& s, const int (&at)[kIds], const uint32_t (&old)[kIds]) {
-  const int lane = threadIdx.x & 31;
-  int n = 0;
-#pragma unroll
-  for (int u = 0; u < kIds; ++u) n += old[u] == 0;
-  int before = n;  // places of the lanes up to this one
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int other = __shfl_up_sync(kFull, before, o);
-    if (lane >= o) before += other;
-  }
-  const int all = __shfl_sync(kFull, before, 31);
-  if (!all) return;
-  int pos = 0;
-  if (lane == 31) pos = atomicAdd(&s.n_list, all);
-  pos = __shfl_sync(kFull, pos, 31) + before - n;
-#pragma unroll
-  for (int u = 0; u < kIds; ++u)
-    if (old[u] == 0) s.list[pos++] = uint16_t(at[u]);
 }
 
 // 1 x 151936 fp32 with everything: 8 us, of which a launch and its merge are 4.
@@ -362,19 +333,11 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
     // Count the history; mark what the biases name.
     for (int base = 0; base < len; base += kIdsBlock) {
       if (base) ids.load(base, len, span, ids_at);
-      uint32_t old[kIds];
-      bool any = false;
 #pragma unroll
       for (int u = 0; u < kIds; ++u) {
         const int i = base + u * kRowThreads + int(threadIdx.x);
-        if (i >= len) ids_at[u] = -1;
-        any |= ids_at[u] >= 0;
+        count_id(s, i < len ? ids_at[u] : -1, i >= prompt);
       }
-      if (!__any_sync(kFull, any)) continue;
-#pragma unroll
-      for (int u = 0; u < kIds; ++u)
-        old[u] = count_id(&s.table[max(ids_at[u], 0)], ids_at[u] >= 0, base + u * kRowThreads + int(threadIdx.x) < prompt);
-      append(s, ids_at, old);
     }
     auto name = [&](int at) {
       if (at >= 0) {
@@ -387,25 +350,35 @@ __global__ void __launch_bounds__(kRowThreads, V * NV > 16 ? 3 : 4) process_logi
     for (int i = kBiases * kRowThreads + threadIdx.x; i < p.n_bias; i += kRowThreads) name(bias_ids.one(i, span));
     __syncthreads();
 
-    // One thread per listed place works out its value from the logit (in L1:
-    // the tile's loads have just passed there).
-    const int n = s.n_list;
+    // A warp lists the places of its words of the map (every eighth, as marks may
+    // crowd), and a lane per place works out its value from the logit (in L1: the
+    // tile's loads have just passed there).
+    const int lane = threadIdx.x & 31, word = lane * kRowWarps + (threadIdx.x >> 5);
+    uint32_t places = word < kTile / 32 ? s.map[word] : 0u;
+    int upto = __popc(places);  // places of the lanes up to this one
+    int pos = -upto;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int other = __shfl_up_sync(kFull, upto, o);
+      if (lane >= o) upto += other;
+    }
+    pos += upto;
+    const int n = __shfl_sync(kFull, upto, 31);
+    uint16_t* list = s.list + (threadIdx.x >> 5) * (kTile / kRowWarps);
+    for (; places; places &= places - 1) list[pos++] = uint16_t(word * 32 + __ffs(places) - 1);
+    __syncwarp();
     constexpr int kLoads = 4;  // under way at once
-    for (int base = threadIdx.x; base < n; base += kRowThreads * kLoads) {
+    for (int base = lane; base < n; base += 32 * kLoads) {
       int at[kLoads];
       float z[kLoads];
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) {
-        const int i = base + u * kRowThreads;
-        at[u] = i < n ? int(s.list[i]) : -1;
+        at[u] = base + u * 32 < n ? int(list[base + u * 32]) : -1;
         if (at[u] >= 0) z[u] = to_f32(logits[first + at[u]]);
       }
 #pragma unroll
       for (int u = 0; u < kLoads; ++u)
-        if (at[u] >= 0) {
-          s.table[at[u]] = __float_as_uint(penalise(z[u], s.table[at[u]], rep, pres, freq, has_rep));
-          mark(s.map, at[u]);
-        }
+        if (at[u] >= 0) s.table[at[u]] = __float_as_uint(penalise(z[u], s.table[at[u]], rep, pres, freq, has_rep));
     }
     __syncthreads();
     if (s.biased) {
