@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t abs_bits(float y) { return __float_as_uint(y
 // before its squares are summed, as the backward reads it rounded.
 // 16384 x 4096 bf16 with residual: 81.6 us, 6.6 TB/s, what a copy reaches; one
 // row of 4096: 3.4 us, a launch.  With the 8-bit output and groups of 128, 8192 x
-// 2048 fp16 takes 28 us for 118 MB (4.2 TB/s): groups' maxima, the division by
+// 2048 fp16 takes 26.7 us for 118 MB (4.4 TB/s): groups' maxima, the division by
 // the scale and the conversion bring it to about 35 instructions per element, and
 // issue slots are the bound.
 template <class T, class R, int V, int NV, RowForm kForm, bool kRagged, bool kFp8>
