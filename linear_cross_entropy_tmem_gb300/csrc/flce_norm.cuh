@@ -240,6 +240,20 @@ struct RowVectors {
     if constexpr (V == 1) return reinterpret_cast<float*>(slots) + i * width + thread;
     return reinterpret_cast<float*>(slot<16>(slots, i * (V / 4) + k / 4)) + k % 4;
   }
+  // Vector i of such a region, for sums.
+  __device__ __forceinline__ void put(uint8_t* slots, int i, const Floats<V>& f) const {
+    if constexpr (V == 1) {
+      float lo, hi;
+      f2_unpack(f.p[0], lo, hi);
+      *weight_at(slots, i, 0) = lo;
+    } else {
+#pragma unroll
+      for (int c = 0; c < V / 4; ++c) {
+        ulonglong2 two = {f.p[2 * c], f.p[2 * c + 1]};
+        *reinterpret_cast<ulonglong2*>(slot<16>(slots, i * (V / 4) + c)) = two;
+      }
+    }
+  }
   __device__ __forceinline__ Floats<V> weight(uint8_t* slots, int i) const {
     Vec<float, V> x;
     if constexpr (V == 1) {

@@ -12,10 +12,17 @@ namespace {
 // dweight nothing but the rows' traffic is left.  What is above the copy rate:
 // one wave of blocks (more waves mean more partial rows), the partial rows and
 // the reduction's launch.
+// Where one block fills an SM nobody hides its waits, so rstd is loaded a row
+// ahead too (8192 x 8192: 86 us, not ahead 108; the forms with more blocks lose by
+// it, 8 us of 88 at 16384 x 2048 with an fp32 residual).  The widest rows leave
+// no registers for the dweight sums: in shared memory, 4096 x 16384 takes 214 us
+// in place of 259.
 template <class T, class R, int V, int NV, RowForm kForm, bool kRagged>
 __global__ void __launch_bounds__(row_threads(kForm), bwd_blocks(kForm, kRagged, V * NV)) norm_bwd_kernel(NormBwdParams p) {
   constexpr bool kWarpRow = kForm == kWarp;
   constexpr bool kCopy = copies(kForm, V);  // rows are copied ahead
+  constexpr bool kOne = kForm == kWide || kForm == kBig;  // one block on an SM: nobody hides its waits
+  constexpr bool kSumsSmem = kForm == kBig;               // no registers left for them
   extern __shared__ __align__(16) uint8_t smem[];  // weights and slots; later, kWarpRow: [cols] sums
   __shared__ float red[2][32];
   griddep_release();  // the reduction of dweight may be set up
@@ -56,15 +63,20 @@ __global__ void __launch_bounds__(row_threads(kForm), bwd_blocks(kForm, kRagged,
     if (row < p.rows) edges();
   }
   at.keep_weights(p.w, p.w_dtype, p.offset, weights);
+  uint8_t* sums = smem + at.template bytes<float>();  // kSumsSmem: behind the weights, laid out alike
   Floats<V> acc[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
 #pragma unroll
     for (int j = 0; j < acc[i].kPairs; ++j) acc[i].p[j] = f2_splat(0.f);
+    if (kSumsSmem) at.put(sums, i, acc[i]);
+  }
   int turn = 0, stage = 0;
   const float inv_cols = 1.0f / float(p.cols);
+  float rstd_next = kOne && row < p.rows ? p.rstd[row] : 0.f;  // a row ahead
   for (; row < p.rows; row += step) {
-    const float rstd = p.rstd[row];
+    const float rstd = kOne ? rstd_next : p.rstd[row];
+    if (kOne && row + step < p.rows) rstd_next = p.rstd[row + step];
     if constexpr (kCopy) {
       cp_async_wait<kRowStages - 1>();
     } else {
@@ -86,6 +98,7 @@ __global__ void __launch_bounds__(row_threads(kForm), bwd_blocks(kForm, kRagged,
         if (p.dh) dhv = at.read(from + dh_at, i, dhe);
       }
       const Floats<V> w = at.weight(weights, i), d = widen(dyv), hf = widen(hv);
+      if (kSumsSmem) acc[i] = at.weight(sums, i);
 #pragma unroll
       for (int j = 0; j < w.kPairs; ++j) {
         n[i].p[j] = f2_mul(hf.p[j], rstd2);
@@ -93,6 +106,7 @@ __global__ void __launch_bounds__(row_threads(kForm), bwd_blocks(kForm, kRagged,
         dots = f2_fma(a[i].p[j], n[i].p[j], dots);
         acc[i].p[j] = f2_fma(d.p[j], n[i].p[j], acc[i].p[j]);
       }
+      if (kSumsSmem) at.put(sums, i, acc[i]);
       if (p.dh) {
         const Floats<V> e = widen(dhv);
 #pragma unroll
@@ -124,12 +138,14 @@ __global__ void __launch_bounds__(row_threads(kForm), bwd_blocks(kForm, kRagged,
   if (!p.part) return;
   float sum[NV][V];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    if (kSumsSmem) acc[i] = at.weight(sums, i);
 #pragma unroll
     for (int j = 0; j < acc[i].kPairs; ++j) {
       float hi;
       f2_unpack(acc[i].p[j], sum[i][2 * j], V == 1 ? hi : sum[i][V == 1 ? 0 : 2 * j + 1]);
     }
+  }
   float* part = p.part + int64_t(blockIdx.x) * p.cols;
   if (kWarpRow) {  // the warps add their sums in warp order
     float* dw_s = reinterpret_cast<float*>(smem);
@@ -205,7 +221,8 @@ cudaError_t launch_bwd(const NormBwdParams& p, const RowPlan& pl, int blocks, cu
   auto kern = pick_form<V>(pl, [](auto nv, auto form, auto ragged) {
     return &norm_bwd_kernel<T, R, V, decltype(nv)::value, decltype(form)::value, decltype(ragged)::value>;
   });
-  const int slots = row_smem(pl, sizeof(T) + 2 * sizeof(R));
+  const int sums = pl.form == kBig ? pl.threads * pl.nv * pl.vec * 4 : 0;
+  const int slots = row_smem(pl, sizeof(T) + 2 * sizeof(R)) + sums;
   const int smem = std::max(slots, pl.form == kWarp ? p.cols * 4 : 0);
   if (smem > 47 * 1024) {  // the kernels also have some of their own
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

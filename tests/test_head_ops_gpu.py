@@ -730,3 +730,12 @@ def test_host_memory_is_refused_before_any_launch(lib):
                                        1 << 16, None) == B.FLCE_ERR_INVALID_ARG
     assert lib.flce_testing_launch_count() == before
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("types", [(BF, BF), (HF, SP), (SP, SP)])
+@pytest.mark.parametrize("rows,cols", [(500, 9001), (333, 16384), (320, 8200)])
+def test_norm_backward_wide_many_rows(rows, cols, types):
+    """Several wide rows per block: their dweight sums wait in shared memory."""
+    t, rt = types
+    dy, h, dh = rand((rows, cols), t, 1), rand((rows, cols), rt, 2, 2.0), rand((rows, cols), rt, 3)
+    check_backward(dy, h, rand((cols,), t, 4), dh)
