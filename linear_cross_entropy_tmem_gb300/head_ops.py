@@ -20,6 +20,7 @@ from functools import lru_cache
 from typing import Iterable, NamedTuple, Optional, Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as B
 
@@ -233,7 +234,8 @@ def flce_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Te
 
 class AddRmsNorm(torch.autograd.Function):
     """Autograd wrapper: ``(y, h)`` of x and an optional residual.  The gradients of x and of the residual are
-    the same values; the backward forms what is asked for."""
+    the same values; the backward forms what is asked for.  It has no derivative of its own: a second backward
+    through the gradients raises."""
 
     @staticmethod
     def forward(ctx, x, weight, residual, eps, weight_offset):
@@ -250,6 +252,7 @@ class AddRmsNorm(torch.autograd.Function):
         return r.y, r.h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh=None):
         h, weight, rstd = ctx.saved_tensors
         nx, nw, nr = ctx.needs_input_grad[:3]
