@@ -20,9 +20,9 @@ from functools import lru_cache
 from typing import Iterable, NamedTuple, Optional, Sequence
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import binding as B
+from .once import once
 
 _DTYPES = {torch.float32: B.FLCE_F32, torch.bfloat16: B.FLCE_BF16, torch.float16: B.FLCE_F16}
 
@@ -252,7 +252,6 @@ class AddRmsNorm(torch.autograd.Function):
         return r.y, r.h
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dy, dh=None):
         h, weight, rstd = ctx.saved_tensors
         nx, nw, nr = ctx.needs_input_grad[:3]
@@ -263,7 +262,11 @@ class AddRmsNorm(torch.autograd.Function):
         g = flce_add_rms_norm_backward(_adjacent(dy), h, rstd, weight, dh=None if dh is None else _adjacent(dh),
                                        weight_offset=ctx.offset, need_dx=nx, need_dresidual=nr and ctx.has_residual,
                                        need_dweight=nw)
-        return g.dx, g.dweight, g.dresidual, None, None
+        # what the gradients depend on: h only where it has a gradient itself
+        stream = h if nx or nr else None
+        d = (dy, dh, stream, weight)
+        return (once("add_rms_norm", g.dx, *d), once("add_rms_norm", g.dweight, dy, stream),
+                once("add_rms_norm", g.dresidual, *d), None, None)
 
 
 def _adjacent(t: torch.Tensor) -> torch.Tensor:

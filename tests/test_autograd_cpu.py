@@ -50,5 +50,17 @@ def test_norm_second_derivatives_are_refused(norm_stand_ins, residual, of):
     y = head_ops.add_rms_norm(x, w, r)[0] if residual else head_ops.add_rms_norm(x, w)
     u = torch.linspace(-1.0, 1.0, 8, dtype=torch.float64)
     g, = torch.autograd.grad((y * u).sum(), (x, w)[of], create_graph=True)  # the gradient itself may be had
-    with pytest.raises(RuntimeError, match="once_differentiable"):
+    with pytest.raises(RuntimeError, match="differentiable once"):
         (g.square().sum() + x.sum()).backward()
+
+
+def test_norm_gradients_that_are_constants(norm_stand_ins):
+    """Where only the weight has a gradient, dweight does not depend on it: nothing to refuse.  And a backward without
+    create_graph ties nothing."""
+    x, w, r = _leaves()
+    y, _ = head_ops.add_rms_norm(x.detach(), w, r.detach())
+    g, = torch.autograd.grad(y.sum(), w, create_graph=True)
+    assert not g.requires_grad
+    y, h = head_ops.add_rms_norm(x, w, r)
+    (y.sum() + h.sum()).backward()
+    assert all(t.grad.grad_fn is None and not t.grad.requires_grad for t in (x, w, r))
