@@ -12,6 +12,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import binding as B
+from .once import once
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -242,7 +243,9 @@ class LinearCrossEntropy(torch.autograd.Function):
     through the same graph recomputes them (``flce_backward``) instead of rescaling.
 
     When neither the weight nor the bias requires a gradient (a frozen head, e.g. LoRA training),
-    only dhidden is formed (``FLCE_FLAG_FROZEN_HEAD``)."""
+    only dhidden is formed (``FLCE_FLAG_FROZEN_HEAD``).
+
+    The gradients have no derivative of their own: a second backward through them raises."""
 
     @staticmethod
     def forward(ctx, hidden, weight, bias, targets, logit_scale, softcap, ignore_index, reduction,
@@ -275,6 +278,9 @@ class LinearCrossEntropy(torch.autograd.Function):
         else:
             hidden, weight, bias, targets, lse, n_valid = ctx.saved_tensors
             dh, dW, db = flce_backward(hidden, weight, targets, lse, n_valid, dloss.contiguous(), bias, **ctx.cfg)
+        if torch.is_grad_enabled():  # create_graph
+            sources = (dloss, *ctx.saved_tensors[:3])
+            dh, dW, db = (once("linear_cross_entropy", x, *sources) for x in (dh, dW, db))
         return dh, dW, db, None, None, None, None, None, None, None, None, None
 
 
