@@ -133,6 +133,11 @@ bool workspace(PyObject* o, size_t bytes, const Tensor& like, Tensor* out) {
   *out = *a.t;
   return a->is_contiguous() && size_t(a->numel()) * a->element_size() >= bytes;
 }
+// The call has written a tensor of the caller's: autograd has to know (a backward that saved it raises, as after any
+// in-place operation of torch).  Inference tensors keep no count.
+void wrote(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 bool vector_of(const Arg& a, int64_t n, at::ScalarType t) {
   return a->dim() == 1 && a->size(0) == n && a->scalar_type() == t && a->is_contiguous();
 }
@@ -287,6 +292,7 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
             : g_entry.grad_norm(src.data(), numel.data(), dtype.data(), count, out, ws.data_ptr(), bytes,
                                 stream_of(like));
   if (rc != FLCE_OK) return status(rc);
+  for (Py_ssize_t i = 0; clip && i < count; ++i) wrote(THPVariable_Unpack(to ? os[i] : gs[i]));
   return pack({norm});
   END_HANDLE_TH_ERRORS
 }
@@ -369,6 +375,7 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
                       out.numel() ? out.data_ptr() : nullptr, b ? token.mutable_data_ptr<int64_t>() : nullptr,
                       b ? lse.mutable_data_ptr<float>() : nullptr, ws.data_ptr(), bytes, stream_of(*z.t));
   if (rc != FLCE_OK) return status(rc);
+  if (out_arg) wrote(out);
   PyObject* r = pack({out, token, lse});
   if (r && out_arg) {  // the caller's own object
     Py_INCREF(a[10]);

@@ -20,6 +20,7 @@ from functools import lru_cache
 from typing import Iterable, NamedTuple, Optional, Sequence
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import binding as B
 from .once import once
@@ -164,7 +165,8 @@ def flce_add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                       residual: Optional[torch.Tensor] = None, *, eps: float = 1e-6, weight_offset: float = 0.0,
                       need_rstd: bool = True) -> AddRmsNormResult:
     """Forward of the residual addition and norm over the last dimension (see ``flce_add_rms_norm`` in
-    include/flce.h); ``need_rstd=False`` where no backward follows."""
+    include/flce.h); ``need_rstd=False`` where no backward follows.  Its results carry no gradient:
+    :func:`add_rms_norm` is the call for autograd."""
     out = _call("add_rms_norm", x, weight, residual, eps, weight_offset, bool(need_rstd), -1)
     if out is None:
         out = _norm_forward(x, weight, residual, eps, weight_offset, rstd=need_rstd)
@@ -175,7 +177,7 @@ def flce_add_rms_norm_fp8(x: torch.Tensor, weight: Optional[torch.Tensor] = None
                           residual: Optional[torch.Tensor] = None, *, eps: float = 1e-6, weight_offset: float = 0.0,
                           group: int = 128) -> AddRmsNormFp8Result:
     """The forward with an e4m3 output and one fp32 scale per ``group`` columns of a row (0: per row; see
-    ``flce_add_rms_norm_fp8``)."""
+    ``flce_add_rms_norm_fp8``).  Its results carry no gradient."""
     if not 0 <= group <= 1 << 20:
         raise ValueError(f"flce: group must be 0 or a multiple of 16, got {group}")
     out = _call("add_rms_norm", x, weight, residual, eps, weight_offset, False, int(group))
@@ -356,7 +358,8 @@ def clip_grad_norm_(grads: Iterable[torch.Tensor], max_norm: float, *,
     """Scale ``grads`` by min(1, max_norm / (norm + 1e-6)) in place, or into ``outputs`` (tensors of the same
     dtypes and layouts, such as slices of an optimizer's flat buffer), and return the norm before clipping as a
     0-dim fp32 device tensor (see ``flce_clip_grad_norm``).  Nothing waits for the device.  List no gradient twice,
-    and none that overlaps another: they are scaled side by side."""
+    and none that overlaps another: they are scaled side by side.  Nothing is recorded for autograd; what is written
+    counts as changed in place, so that a backward that saved it raises."""
     grads = list(grads)
     outputs = None if outputs is None else list(outputs)
     max_norm = float(max_norm)
@@ -370,6 +373,8 @@ def clip_grad_norm_(grads: Iterable[torch.Tensor], max_norm: float, *,
     norm = torch.empty((), dtype=torch.float32, device=dev)
     B.check(B.load().flce_clip_grad_norm(src, dst, numel, codes, n, max_norm, norm.data_ptr(), ws.data_ptr(), nbytes,
                                          _stream(dev)), "flce_clip_grad_norm")
+    for t in grads if outputs is None else outputs:
+        increment_version(t)
     return norm
 
 
@@ -411,7 +416,10 @@ def process_logits(logits: torch.Tensor, *, tokens: Optional[torch.Tensor] = Non
     ``tokens`` [B, H]: each request's history, of which the first ``lens[b]`` columns count and the first
     ``prompt_lens[b]`` are its prompt; ``repetition``, ``presence``, ``frequency`` [B] fp32.  ``bias_ids`` and
     ``bias`` [B, K]: sparse additions.  Ids outside [0, V) are padding.  ``mask`` [B, ceil(V / 32)] int32: bit
-    v % 32 of word v // 32 allows entry v.  ``out`` may be ``logits``; ``out_dtype`` is logits' dtype or fp32."""
+    v % 32 of word v // 32 allows entry v.  ``out`` may be ``logits``; ``out_dtype`` is logits' dtype or fp32.
+
+    Nothing is recorded for autograd: the results carry no gradient, whatever the logits do, and a given ``out`` counts
+    as changed in place, so that a backward that saved it raises."""
     res = _call("process_logits", logits, tokens, lens, prompt_lens, repetition, presence, frequency, bias_ids, bias,
                 mask, out, -1 if out_dtype is None else _code(out_dtype, "out"), workspace)
     if res is not None:
@@ -448,7 +456,8 @@ def process_logits(logits: torch.Tensor, *, tokens: Optional[torch.Tensor] = Non
             raise ValueError(f"flce: mask must be int32 of shape {(b, (v + 31) // 32)}")
         mask = _rows(mask, "mask")
         ms = mask.stride(0)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((b, v), dtype=out_dtype or logits.dtype, device=dev)
     elif out.shape != logits.shape or (out_dtype is not None and out.dtype != out_dtype) or \
             (v > 1 and out.stride(1) != 1):
@@ -470,4 +479,6 @@ def process_logits(logits: torch.Tensor, *, tokens: Optional[torch.Tensor] = Non
                                     _addr(repetition), _addr(presence), _addr(frequency), _addr(bias_ids),
                                     _addr(bias), _addr(mask), _addr(out), _addr(token), _addr(lse), _addr(ws),
                                     size.value, _stream(dev)), "flce_process_logits")
+    if given:
+        increment_version(out)
     return ProcessedLogits(out, token, lse)

@@ -1,0 +1,63 @@
+"""What the torch calls on either side of the head owe torch: counts of in-place changes, and the same results whether
+the tensors are marshalled natively or in Python."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import linear_cross_entropy_tmem_gb300 as F
+from linear_cross_entropy_tmem_gb300 import head_ops
+
+pytestmark = pytest.mark.gpu
+
+BF, SP = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(params=["native", "python"])
+def path(request, monkeypatch):
+    if request.param == "python":
+        monkeypatch.setattr(head_ops, "_call", lambda *a: None)
+    return request.param
+
+
+def test_a_saved_tensor_that_a_call_wrote_raises_in_backward(path):
+    z = torch.randn(3, 100, device="cuda", requires_grad=True)
+    logits = z * 1.0
+    loss = logits.exp().sum()  # saves its result
+    used = logits.square().sum()  # saves logits
+    F.process_logits(logits, out=logits)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        used.backward()
+    loss.backward()  # its saved tensor was not written
+    p = torch.randn(50, device="cuda", requires_grad=True)
+    g = p * 2.0
+    loss = g.square().sum()
+    with torch.no_grad():
+        F.clip_grad_norm_([g], 1e-3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_counts_of_in_place_changes(path):
+    """One for what is written, none for what is read or for a tensor that the call made; a view's base counts with it;
+    inference tensors, which keep no count, are taken."""
+    z, out, flat = torch.randn(4, 64, device="cuda"), torch.empty(4, 64, device="cuda"), torch.empty(200, device="cuda")
+    g = [torch.randn(10, 10, device="cuda"), torch.randn(7, device="cuda"), torch.empty(0, device="cuda")]
+    all_of = lambda: [t._version for t in (z, out, flat, *g)]  # noqa: E731
+    start = all_of()
+    since = lambda: [a - b for a, b in zip(all_of(), start)]  # noqa: E731
+    F.process_logits(z)
+    F.grad_norm(g)
+    assert since() == [0] * 6
+    assert F.process_logits(z, out=out).logits is out
+    assert since() == [0, 1, 0, 0, 0, 0]
+    F.process_logits(z, out=z)
+    assert since() == [1, 1, 0, 0, 0, 0]
+    F.clip_grad_norm_(g, 1.0, outputs=[flat[:100].view(10, 10), flat[100:107], flat[:0]])
+    assert since() == [1, 1, 3, 0, 0, 0]
+    F.clip_grad_norm_(g, 1.0)
+    assert since() == [1, 1, 3, 1, 1, 1]
+    with torch.inference_mode():
+        t = torch.randn(4, 64, device="cuda")
+        F.process_logits(t, out=t)
+        F.clip_grad_norm_([t], 1.0)
