@@ -10,6 +10,7 @@ import ctypes
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import binding as B
 from .once import once
@@ -135,7 +136,7 @@ def flce_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
                   fp32_full: bool = False, frozen_head: bool = False, workspace: Optional[torch.Tensor] = None,
                   outputs=None):
     """Backward (see ``flce_backward`` in include/flce.h); returns (dhidden, dweight, dbias), with
-    dweight and dbias None for a frozen head."""
+    dweight and dbias None for a frozen head.  Given ``outputs`` count as changed in place."""
     _require_cuda(hidden, weight, targets, lse, n_valid, dloss, bias)
     for t, n in ((hidden, "hidden"), (weight, "weight"), (targets, "targets"), (bias, "bias"), (lse, "lse")):
         _contig(t, n)
@@ -160,6 +161,9 @@ def flce_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
                                 _ptr(lse), _ptr(n_valid), _ptr(dloss), _ptr(dh), _ptr(dW), _ptr(db), _ptr(ws),
                                 ws.numel(), _stream(dev))
     B.check(st, "flce_backward")
+    for t in outputs or ():
+        if t is not None:
+            increment_version(t)
     return dh, dW, db
 
 
@@ -223,12 +227,14 @@ def flce_status_string(status: int) -> str:
 
 def scale_gradient(x: torch.Tensor, scale: torch.Tensor) -> torch.Tensor:
     """``x *= scale`` in place on the device (see ``flce_scale_gradient``); ``scale`` is a one-element
-    fp32 device tensor, and nothing is read or written when it holds exactly 1."""
+    fp32 device tensor, and nothing is read or written when it holds exactly 1.  Nothing is recorded for autograd; ``x``
+    counts as changed in place either way."""
     _require_cuda(x, scale)
     _contig(x, "x")
     scale = scale.to(dtype=torch.float32).contiguous().reshape(-1)[:1]
     B.check(B.load().flce_scale_gradient(_ptr(scale), _ptr(x), x.numel(), _dtype_code(x.dtype, "x"),
                                          _stream(x.device)), "flce_scale_gradient")
+    increment_version(x)
     return x
 
 

@@ -61,3 +61,22 @@ def test_counts_of_in_place_changes(path):
         t = torch.randn(4, 64, device="cuda")
         F.process_logits(t, out=t)
         F.clip_grad_norm_([t], 1.0)
+
+
+def test_what_the_loss_calls_write_counts_as_changed():
+    h, w, b = (torch.randn(s, device="cuda").to(BF) for s in ((40, 64), (100, 64), (100,)))
+    t = torch.randint(0, 100, (40,), device="cuda")
+    f = F.flce_forward(h, w, t, b)
+    outs = tuple(torch.empty_like(x) for x in (h, w, b))
+    start = [x._version for x in (h, w, b, *outs)]
+    got = F.flce_backward(h, w, t, f.lse, f.n_valid, torch.ones(1, device="cuda"), b, outputs=outs)
+    assert all(a is o for a, o in zip(got, outs))
+    assert [x._version - s for x, s in zip((h, w, b, *outs), start)] == [0, 0, 0, 1, 1, 1]
+    F.scale_gradient(outs[0], torch.full((1,), 0.5, device="cuda"))
+    assert outs[0]._version == start[3] + 2
+    p = torch.randn(50, device="cuda", requires_grad=True)
+    g = p * 2.0
+    loss = g.square().sum()
+    F.scale_gradient(g, torch.full((1,), 0.5, device="cuda"))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
