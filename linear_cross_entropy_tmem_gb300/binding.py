@@ -11,7 +11,17 @@ import os
 from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libflce.so")
-TORCH_PATH = os.path.join(os.path.dirname(LIB_PATH), "flce_torch.so")
+
+
+def torch_path() -> str:
+    """The native marshalling's file.  It is compiled against one torch and one Python, which its name says: under
+    another it is not found, rather than loaded."""
+    import sysconfig
+
+    import torch
+    return os.path.join(os.path.dirname(LIB_PATH),
+                        f"flce_torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
 
 FLCE_F32, FLCE_BF16, FLCE_F16 = 0, 1, 2
 FLCE_RED_NONE, FLCE_RED_SUM, FLCE_RED_MEAN = 0, 1, 2
@@ -177,7 +187,7 @@ def load(path: str = LIB_PATH):
     return lib
 
 
-# What flce_torch.so calls, in the order of its table.
+# What flce_torch calls, in the order of its table.
 _MARSHALLED = ("flce_add_rms_norm", "flce_add_rms_norm_fp8", "flce_add_rms_norm_workspace_size",
                "flce_add_rms_norm_backward", "flce_grad_norm_workspace_size", "flce_grad_norm", "flce_clip_grad_norm",
                "flce_process_logits_workspace_size", "flce_process_logits")
@@ -185,15 +195,16 @@ _TORCH = None
 
 
 def load_torch():
-    """Load ``flce_torch.so``, the native marshalling of torch tensors, on the loaded library's functions."""
+    """Load ``flce_torch``, the native marshalling of torch tensors, on the loaded library's functions."""
     global _TORCH
     if _TORCH is None:
         import importlib.machinery
         import importlib.util
         lib = load()
-        if not os.path.exists(TORCH_PATH):
-            raise RuntimeError(f"flce_torch.so not found at {TORCH_PATH}: build it with __graft_entry__.build()")
-        loader = importlib.machinery.ExtensionFileLoader("flce_torch", TORCH_PATH)
+        path = torch_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"flce_torch not found at {path}: build it with __graft_entry__.build()")
+        loader = importlib.machinery.ExtensionFileLoader("flce_torch", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("flce_torch", loader))
         loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, name), c_void_p).value for name in _MARSHALLED))

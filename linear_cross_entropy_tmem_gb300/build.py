@@ -1,9 +1,10 @@
-"""In-tree build of ``libflce.so`` for sm_103a with nvcc (no cmake, no setuptools), and of ``flce_torch.so``, the
+"""In-tree build of ``libflce.so`` for sm_103a with nvcc (no cmake, no setuptools), and of ``flce_torch``, the
 native marshalling of torch tensors, with the host compiler.
 
-The translation units compile in parallel; the outputs are rebuilt only when a
-source or header is newer than they are.  Output:
-``linear_cross_entropy_tmem_gb300/_build/``.
+The translation units compile in parallel; each output is rebuilt only when a
+source or header is newer than it is.  The library does not depend on the
+marshalling: it is linked also where that does not compile, which is then
+raised.  Output: ``linear_cross_entropy_tmem_gb300/_build/``.
 
     python -m linear_cross_entropy_tmem_gb300.build
 """
@@ -16,6 +17,8 @@ import shutil
 import subprocess
 import sys
 
+from .binding import torch_path
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
@@ -25,7 +28,6 @@ LIB = os.path.join(BUILD, "libflce.so")
 SOURCES = ["flce_api.cu", "flce_fwd.cu", "flce_bwd.cu", "flce_noalloc.cu", "flce_norm.cu", "flce_norm_fwd.cu", "flce_norm_fp8.cu",
            "flce_norm_bwd.cu", "flce_clip.cu", "flce_logits.cu"]
 TORCH_SOURCE = "flce_torch.cpp"
-TORCH_LIB = os.path.join(BUILD, "flce_torch.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -41,10 +43,11 @@ def _flags():
             f"-I{INCLUDE}", f"-I{CSRC}"]
 
 
-def _newest_input() -> float:
+def _stale(output: str) -> bool:
+    """Whether ``output`` is missing or older than a source or header."""
     files = glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     files.append(os.path.abspath(__file__))
-    return max(os.path.getmtime(f) for f in files)
+    return not os.path.exists(output) or os.path.getmtime(output) < max(os.path.getmtime(f) for f in files)
 
 
 def _compile(src: str) -> str:
@@ -56,15 +59,15 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _compile_torch() -> str:
-    """flce_torch.so: a Python extension on torch's C++ interface."""
+def _compile_torch(out: str) -> None:
+    """flce_torch: a Python extension on torch's C++ interface."""
     import sysconfig
 
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-    tmp = TORCH_LIB + ".tmp"
+    tmp = out + ".tmp"
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}", f"-isystem{inc}",
            f"-isystem{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-isystem{cuda}",
@@ -73,28 +76,30 @@ def _compile_torch() -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {TORCH_SOURCE}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, TORCH_LIB)
-    return TORCH_LIB
+    os.replace(tmp, out)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Build (or reuse) libflce.so and return its path."""
-    os.makedirs(BUILD, exist_ok=True)
-    newest = _newest_input()
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, TORCH_LIB)):
-        return LIB
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        marshal = ex.submit(_compile_torch)
-        objs = list(ex.map(_compile, SOURCES))
-        marshal.result()
+def _link(objs) -> None:
     tmp = LIB + ".tmp"
     cmd = [nvcc(), ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    if verbose:
-        print(f"built {LIB}")
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Build (or reuse) libflce.so and flce_torch, and return the library's path."""
+    os.makedirs(BUILD, exist_ok=True)
+    torch_lib = torch_path()
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_compile_torch, torch_lib) if force or _stale(torch_lib) else None
+        if force or _stale(LIB):
+            _link(list(ex.map(_compile, SOURCES)))
+            if verbose:
+                print(f"built {LIB}")
+        if marshal is not None:
+            marshal.result()
     return LIB
 
 

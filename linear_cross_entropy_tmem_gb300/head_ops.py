@@ -9,7 +9,7 @@
 As in ``api.py``, PyTorch provides device memory and the current stream, every step runs in
 ``libflce.so``, and there is no CPU path.  See ``include/flce.h`` for the formulas.
 
-Tensors that are as the library wants them are marshalled by ``flce_torch.so`` (a step of one token
+Tensors that are as the library wants them are marshalled by ``flce_torch`` (a step of one token
 is shorter than reading its tensors' fields from Python); it returns None for the others, which the
 code here views as rows, or refuses.
 """
