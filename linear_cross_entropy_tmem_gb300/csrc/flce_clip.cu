@@ -16,7 +16,6 @@
 // per 32 elements and fp64 sums over the block the first pass ran at half the
 // memory's rate (head: 1021 us; 34 M fp32 elements: 95, now 72).  So a chunk is summed in fp32, compensated over its rounds, and
 // only chunks whose squares leave fp32's safe range are summed again in fp64.
-#include <algorithm>
 #include <cmath>
 
 #include "flce_device.cuh"
@@ -31,7 +30,6 @@ constexpr int kTotalThreads = 1024;
 constexpr int kUnroll = 4;            // 16-byte loads under way per thread
 constexpr int kMinChunk = 8192;       // elements per chunk: this times a power of two,
 constexpr int64_t kWantChunks = 8000; // so that there are about this many at most
-constexpr int kMaxGrid = 32768;       // blocks of a launch at most: partial sums per launch
 constexpr int kFewParts = 512;        // up to here every block of the second pass adds the partial sums itself
 constexpr int kSmallTable = 32;       // tensors per launch: the small table is copied faster
 constexpr int kMediumTable = 240;
@@ -153,35 +151,33 @@ __device__ __forceinline__ double block_tree(double x, double* red) {
   return red[0];
 }
 
-// The first pass: each block adds up chunks and writes one partial sum.  kUnroll
+// The first pass: each block adds up a chunk and writes one partial sum.  kUnroll
 // loads per thread under way and blocks of one chunk keep it at the copy rate;
-// with chunks of about 8000 per call the partial sums stay few.
+// with about 8000 chunks per call, and one more for each tensor, the partial sums
+// stay few.
 template <int N, class T>
 __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_constant__ GradTable<N> t, double* part) {
   __shared__ double red[kGradThreads];
   __shared__ float red32[32];
   griddep_release();  // the next kernel may be set up
-  double all = 0.0;
-  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const int i = find_tensor(t, c);
-    const int64_t begin = int64_t(c - (i ? t.chunk_end[i - 1] : 0)) * t.chunk;
-    const int n = int(min(int64_t(t.chunk), t.numel[i] - begin));
-    const T* p = static_cast<const T*>(t.src[i]) + begin;
-    bool safe = true;
-    float s = chunk_norm(p, n, &safe);
-    if (!__syncthreads_or(!safe)) {
-      s = block_sum(s, red32);
-      all += double(s);
-    } else {
-      double d = 0.0;
-      for (int k = threadIdx.x; k < n; k += kGradThreads) {
-        const double x = double(to_f32(p[k]));
-        d = fma(x, x, d);
-      }
-      all += block_tree(d, red);
+  const int c = blockIdx.x, i = find_tensor(t, c);
+  const int64_t begin = int64_t(c - (i ? t.chunk_end[i - 1] : 0)) * t.chunk;
+  const int n = int(min(int64_t(t.chunk), t.numel[i] - begin));
+  const T* p = static_cast<const T*>(t.src[i]) + begin;
+  bool safe = true;
+  const float s = chunk_norm(p, n, &safe);
+  double all;  // of the chunk's squares
+  if (!__syncthreads_or(!safe)) {
+    all = double(block_sum(s, red32));
+  } else {
+    double d = 0.0;
+    for (int k = threadIdx.x; k < n; k += kGradThreads) {
+      const double x = double(to_f32(p[k]));
+      d = fma(x, x, d);
     }
+    all = block_tree(d, red);
   }
-  if (threadIdx.x == 0) part[blockIdx.x] = all;
+  if (threadIdx.x == 0) part[c] = all;
 }
 
 // Sum of the blocks' partial sums; `red` has blockDim.x values.
@@ -275,13 +271,11 @@ __global__ void __launch_bounds__(kGradThreads, 4) grad_scale_kernel(const __gri
   // an infinite limit over an infinite norm is NaN; such a limit clips nothing
   const float c = max_norm == INFINITY && nm == nm ? 1.0f : f;
   // last chunks first: the norm's pass has just read them
-  for (int c0 = t.chunks - 1 - int(blockIdx.x); c0 >= 0; c0 -= gridDim.x) {
-    const int i = find_tensor(t, c0);
-    if (c == 1.0f && t.src[i] == t.dst[i]) continue;
-    const int64_t begin = int64_t(c0 - (i ? t.chunk_end[i - 1] : 0)) * t.chunk;
-    const int n = int(min(int64_t(t.chunk), t.numel[i] - begin));
-    chunk_scale(static_cast<const T*>(t.src[i]) + begin, static_cast<T*>(t.dst[i]) + begin, n, c);
-  }
+  const int c0 = t.chunks - 1 - int(blockIdx.x), i = find_tensor(t, c0);
+  if (c == 1.0f && t.src[i] == t.dst[i]) return;
+  const int64_t begin = int64_t(c0 - (i ? t.chunk_end[i - 1] : 0)) * t.chunk;
+  const int n = int(min(int64_t(t.chunk), t.numel[i] - begin));
+  chunk_scale(static_cast<const T*>(t.src[i]) + begin, static_cast<T*>(t.dst[i]) + begin, n, c);
 }
 
 // ---------------------------------------------------------------------------
@@ -355,9 +349,8 @@ int run_tables(const Grads& g, bool clip, float max_norm, float* norm, double* p
   while (elements / chunk > kWantChunks) chunk *= 2;
   int parts = 0;
   FLCE_TRY(for_tables<N>(g, chunk, st, [&](const GradTable<N>& t, auto type) {
-    const int grid = std::min(t.chunks, kMaxGrid);
-    grad_norm_kernel<N, decltype(type)><<<grid, kGradThreads, 0, st>>>(t, part + parts);
-    parts += grid;
+    grad_norm_kernel<N, decltype(type)><<<t.chunks, kGradThreads, 0, st>>>(t, part + parts);
+    parts += t.chunks;
     return cudaGetLastError();
   }));
   const bool alone = !clip || parts == 0 || parts > kFewParts;
@@ -367,8 +360,8 @@ int run_tables(const Grads& g, bool clip, float max_norm, float* norm, double* p
     }));
   if (!clip || parts == 0) return FLCE_OK;
   return for_tables<N>(g, chunk, st, [&](const GradTable<N>& t, auto type) {
-    return launch_dependent(grad_scale_kernel<N, decltype(type)>, unsigned(std::min(t.chunks, kMaxGrid)), kGradThreads,
-                            st, t, static_cast<const double*>(part), alone ? 0 : parts, max_norm, norm);
+    return launch_dependent(grad_scale_kernel<N, decltype(type)>, unsigned(t.chunks), kGradThreads, st, t,
+                            static_cast<const double*>(part), alone ? 0 : parts, max_norm, norm);
   });
 }
 
