@@ -420,7 +420,9 @@ FLCE_API int flce_add_rms_norm(const flce_norm_problem* problem, const void* x, 
  * Forward whose normalised output is held in 8 bits (e4m3, largest value 448):
  * for each group of quant_group columns of a row (the last may be short)
  *   scale = max_j |y_j| / 448,  q_j = e4m3(y_j / scale), 0 where scale is 0,
- * with y in fp32.  A group with a NaN or an infinity gets a non-finite scale.
+ * with y as real numbers: the quotient (in which rstd cancels) is rounded to fp32
+ * once and then to e4m3.  Only weight_j + weight_offset is rounded before, to fp32.
+ * A group with a NaN or an infinity gets a non-finite scale.
  *   q      [N, D] bytes, y_stride between rows
  *   scale  [N, ceil(D / group)] fp32, dense
  */

@@ -25,8 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libflce.so")
-SOURCES = ["flce_api.cu", "flce_fwd.cu", "flce_bwd.cu", "flce_noalloc.cu", "flce_norm.cu", "flce_norm_fwd.cu", "flce_norm_fp8.cu",
-           "flce_norm_bwd.cu", "flce_clip.cu", "flce_logits.cu"]
+SOURCES = ["flce_api.cu", "flce_fwd.cu", "flce_bwd.cu", "flce_noalloc.cu", "flce_norm.cu", "flce_norm_fwd.cu",
+           "flce_norm_fp8.cu", "flce_norm_fp8_left.cu", "flce_norm_bwd.cu", "flce_clip.cu", "flce_logits.cu"]
 TORCH_SOURCE = "flce_torch.cpp"
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 

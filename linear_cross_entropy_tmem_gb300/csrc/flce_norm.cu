@@ -140,10 +140,10 @@ int forward(const flce_norm_problem* p, const void* x, const void* residual, con
   n.offset = p->weight_offset;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int grid = row_blocks(pl, p->rows, dev.num_sms, fwd_blocks(pl.form, pl.ragged), row_smem(pl, es + er), 4);
-  return logged(FLCE_LAUNCH_OTHER, st, [&] {
-    return fp8 ? launch_norm_fwd_fp8(n, p->dtype, p->residual_dtype, pl, grid, st)
-               : launch_norm_fwd(n, p->dtype, p->residual_dtype, pl, grid, st);
-  });
+  // 16-bit weights (or none) with no offset: their products with a 16-bit h are exact in fp32
+  const bool exact = er == 2 && (!weight || p->weight_dtype != FLCE_F32) && p->weight_offset == 0.f;
+  const auto launch = !fp8 ? launch_norm_fwd : exact ? launch_norm_fwd_fp8_exact : launch_norm_fwd_fp8_left;
+  return logged(FLCE_LAUNCH_OTHER, st, [&] { return launch(n, p->dtype, p->residual_dtype, pl, grid, st); });
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
 // flce_norm.cuh — residual addition + root-mean-square norm: what its forward
-// (flce_norm_fwd.cu, flce_norm_fp8.cu) and backward (flce_norm_bwd.cu) share.
+// (flce_norm_fwd.cu, flce_norm_fp8*.cu) and backward (flce_norm_bwd.cu) share.
 //
 //   h = rn(x + r),  rstd = (mean h^2 + eps)^(-1/2),  y_j = h_j rstd (w_j + o)
 //   d_j = rstd (g_j - n_j c) + dh_j  with g_j = dy_j (w_j + o), n_j = h_j rstd,
@@ -341,7 +341,8 @@ auto pick_form(const RowPlan& pl, F&& make) {
 }
 
 cudaError_t launch_norm_fwd(const NormParams& p, int32_t dt, int32_t rdt, const RowPlan& pl, int grid, cudaStream_t st);
-cudaError_t launch_norm_fwd_fp8(const NormParams& p, int32_t dt, int32_t rdt, const RowPlan& pl, int grid, cudaStream_t st);
+cudaError_t launch_norm_fwd_fp8_exact(const NormParams& p, int32_t dt, int32_t rdt, const RowPlan& pl, int grid, cudaStream_t st);
+cudaError_t launch_norm_fwd_fp8_left(const NormParams& p, int32_t dt, int32_t rdt, const RowPlan& pl, int grid, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormBwdParams& p, int32_t dt, int32_t rdt, const RowPlan& pl, int blocks, cudaStream_t st);
 
 }  // namespace flce

@@ -100,6 +100,27 @@ def test_norm_fp8_several_rows_placed(rows, cols, places, group):
               group)
 
 
+@pytest.mark.parametrize("rows,cols,group", [(8192, 2048, 128), (8192, 2048, 0), (4096, 4096, 32), (40000, 128, 64),
+                                             (16001, 1283, 48), (2500, 8191, 128), (1000, 16384, 128), (300, 33000, 16)])
+@pytest.mark.parametrize("types", [(BF, BF, BF), (HF, HF, HF), (BF, BF, SP), (HF, SP, HF), (SP, SP, SP)],
+                         ids=["bf16", "f16", "bf16-weights-f32", "f16-f32", "f32"])
+def test_norm_fp8_codes_are_the_quotients(types, rows, cols, group):
+    """Every code is that of the quotient in 64 bits rounded to fp32.  The kernel's quotient is within 2^-44 of itself
+    before its one rounding to fp32; to give another code it would have to round to the other side of one of e4m3's
+    borders, for which the chance is below 2^-40 an element, 2^-15 a test."""
+    t, rt, wt = types
+    x, r, w = rand((rows, cols), t, 1), rand((rows, cols), rt, 2, 2.0), rand((cols,), wt, 3)
+    for offset in (0.0, 1.0):
+        if offset:  # multiples of 2^-6: exact when 1 is added
+            w = ((w.float() * 64.0).round() / 64.0).to(wt)
+        got = F.flce_add_rms_norm_fp8(x, w, r, group=group, weight_offset=offset)
+        y, size = norm_ref(got.h, w, offset, 1e-6)[0], group or cols
+        groups = -(-cols // size)
+        top = torch.nn.functional.pad(y, (0, groups * size - cols)).view(rows, groups, size).abs().amax(2)
+        want = codes(y / (top / 448.0).repeat_interleave(size, 1)[:, :cols])
+        assert int((got.q.float() != want).sum()) == 0
+
+
 @pytest.mark.parametrize("rows,cols", ROWS)
 @pytest.mark.parametrize("places", PLACES, ids=["own", "shifted", "single"])
 @pytest.mark.parametrize("types", TYPES, ids=IDS)
