@@ -453,8 +453,9 @@ FLCE_API int flce_grad_norm_workspace_size(int64_t count, size_t* bytes);
 /*
  * The 2-norm of all elements of `count` dense tensors together:
  *   *norm = sqrt(sum over tensors and elements of g^2)   fp32, on the device
- * The squares are summed so that no finite gradient overflows or underflows
- * (fp32 within small groups, fp64 across them and for extreme values).
+ * The squares are summed in fp32, compensated, within a stretch of a tensor, and in
+ * fp64 across stretches and in those with squares outside fp32's range: none
+ * overflows, or vanishes where it counts.  A norm above fp32's largest value is infinite.
  *   grads   host array of device pointers (NULL allowed where numel is 0)
  *   numel   host array of element counts, >= 0
  *   dtypes  host array of FLCE_* types; they may differ
