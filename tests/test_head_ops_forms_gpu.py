@@ -6,6 +6,10 @@ q = (h_j w_j) / max_j |h_j w_j| * 448 the row's rstd cancels, and what is left a
 either side (4 u, and 1 u where an offset is added to the weights), of the scale (1 u) and of the corrected quotient
 (1 u), u = 2^-24: at most 8 u.  So a code other than the definition's may only appear where the quotient lies within
 2^-20 of itself from a border between two codes.
+
+The norm of gradients is within 2^-20: the squares round (1 u), a thread adds 32 of them in eight chains and a tree (6 u),
+its rounds compensated (2 u), and the block in two trees (10 u), fp64 from there on: at most 19 u of the sum, of which
+the root keeps half.
 """
 from __future__ import annotations
 

@@ -80,3 +80,14 @@ def test_what_the_loss_calls_write_counts_as_changed():
     F.scale_gradient(g, torch.full((1,), 0.5, device="cuda"))
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+def test_second_derivatives_raise():
+    h, w, nw = (torch.randn(s, device="cuda").to(BF).requires_grad_(True) for s in ((40, 64), (100, 64), (64,)))
+    t = torch.randint(0, 100, (40,), device="cuda")
+    for y in (F.add_rms_norm(h, nw), F.add_rms_norm(h, nw, h.detach())[0], F.linear_cross_entropy(h, w, t)[0],
+              F.linear_cross_entropy(h, w, t, grad_in_forward=False)[0]):
+        g, = torch.autograd.grad(y.float().sum(), h, create_graph=True)
+        assert torch.isfinite(g.float()).all()
+        with pytest.raises(RuntimeError, match="differentiable once"):
+            (g.float().square().sum() + h.float().sum()).backward()
