@@ -39,7 +39,8 @@ constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxPerThread = 32;       // entries a thread holds, at most: a tile of 8192
 constexpr int kMaxSingles = 16;         // the same without vectors (a mask word per entry takes registers)
-constexpr int64_t kWantBlocks = 456;    // three blocks on each of 152 SMs
+constexpr int64_t kWantBlocks = 456;    // three blocks on each of a GB300's 152 SMs: the workspace's size depends on
+                                        // it, and that query needs no GPU
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int64_t kMaxIds = (int64_t(1) << 30) - 1;  // of a row's history, and of its biases
 

@@ -75,8 +75,8 @@ __device__ __forceinline__ uint32_t abs_bits(float y) { return __float_as_uint(y
 // 16384 x 4096 bf16 with residual: 81.6 us, 6.6 TB/s, what a copy reaches; one
 // row of 4096: 3.4 us, a launch.  With the 8-bit output and groups of 128, 8192 x
 // 2048 fp16 takes 27.4 us for 118 MB (4.3 TB/s): groups' maxima, the quotient and
-// the conversion bring it to about 36 instructions per element, two of three issue
-// slots are busy, and the rest is latency between a row's reduction and its output.
+// the conversion bring it to 40 instructions per element; 70 % of the issue slots are
+// busy, and the rest is latency between a row's reduction and its output.
 // Where what is left of the products is carried along, 16384 x 2048 bf16 with an
 // fp32 residual takes 86 us (from rounded products 64).  Groups that no power of two
 // of lanes makes up, and ragged rows, go through an atomic maximum per element: at
