@@ -105,7 +105,8 @@ def test_norm_fp8_several_rows_placed(rows, cols, places, group):
 
 
 @pytest.mark.parametrize("rows,cols,group", [(8192, 2048, 128), (8192, 2048, 0), (4096, 4096, 32), (40000, 128, 64),
-                                             (16001, 1283, 48), (2500, 8191, 128), (1000, 16384, 128), (300, 33000, 16)])
+                                             (16001, 1283, 48), (2500, 8191, 128), (1000, 16384, 128), (300, 33000, 16),
+                                             (3, 131072, 16)])
 @pytest.mark.parametrize("types", [(BF, BF, BF), (HF, HF, HF), (BF, BF, SP), (HF, SP, HF), (SP, SP, SP)],
                          ids=["bf16", "f16", "bf16-weights-f32", "f16-f32", "f32"])
 def test_norm_fp8_codes_are_the_quotients(types, rows, cols, group):
@@ -123,6 +124,47 @@ def test_norm_fp8_codes_are_the_quotients(types, rows, cols, group):
         top = torch.nn.functional.pad(y, (0, groups * size - cols)).view(rows, groups, size).abs().amax(2)
         want = codes(y / (top / 448.0).repeat_interleave(size, 1)[:, :cols])
         assert int((got.q.float() != want).sum()) == 0
+
+
+@pytest.mark.parametrize("t,wt", [(BF, BF), (BF, SP), (SP, SP)], ids=["bf16", "bf16-weights-f32", "f32"])
+@pytest.mark.parametrize("size", [1e-35, 1e-25, 1e15])
+@pytest.mark.parametrize("cols,group", [(2048, 128), (2048, 0), (1283, 48), (16400, 64)])
+def test_norm_fp8_codes_of_small_and_large_rows(t, wt, size, cols, group):
+    """The same for values whose reciprocals, squares or products come near fp32's ends."""
+    x, w = (rand((40, cols), SP, 1) * size).to(t), rand((cols,), wt, 3)
+    got = F.flce_add_rms_norm_fp8(x, w, None, group=group)
+    y, n = norm_ref(x, w, 0.0, 1e-6)[0], group or cols
+    groups = -(-cols // n)
+    top = torch.nn.functional.pad(y, (0, groups * n - cols)).view(40, groups, n).abs().amax(2)
+    want = codes(y / (top / 448.0).repeat_interleave(n, 1)[:, :cols])
+    assert int((got.q.float() != want).sum()) == 0
+    within(got.scale, top / 448.0, top / 448.0 * 2.0 ** -16, "scale")
+
+
+@pytest.mark.parametrize("t,rt", [(BF, BF), (HF, SP)], ids=["bf16", "f16-f32"])
+@pytest.mark.parametrize("cols,group", [(2048, 128), (2048, 48), (1283, 128), (16400, 128)])
+def test_norm_fp8_groups_without_a_finite_maximum(t, rt, cols, group):
+    x, r, w = rand((5, cols), t, 1), rand((5, cols), rt, 2), rand((cols,), t, 3)
+    clean = F.flce_add_rms_norm_fp8(x, w, r, group=group)
+    x[1, 200] = math.nan           # the whole row
+    x[2, 300] = math.inf           # rstd 0: the infinity's group is NaN, the others are 0
+    w2 = w.clone()
+    w2[70] = math.inf              # that group of every row
+    got = F.flce_add_rms_norm_fp8(x, w, r, group=group)
+    assert torch.isnan(got.scale[1]).all() and torch.isnan(got.q[1].float()).all()
+    at = 300 // group
+    rest = [g for g in range(got.scale.shape[1]) if g != at]
+    assert torch.isnan(got.scale[2, at]) and torch.all(got.scale[2, rest] == 0)
+    q = got.q[2].float()
+    assert torch.isnan(q[300]) and torch.all(torch.cat([q[:at * group], q[(at + 1) * group:]]) == 0)
+    for row in (0, 3, 4):
+        assert torch.equal(got.q[row].view(torch.uint8), clean.q[row].view(torch.uint8))
+        assert torch.equal(got.scale[row], clean.scale[row])
+    got = F.flce_add_rms_norm_fp8(x, w2, r, group=group)
+    at = 70 // group
+    assert not torch.isfinite(got.scale[:, at]).any() and torch.isnan(got.q[0, 70].float())
+    keep = [g for g in range(got.scale.shape[1]) if g != at]
+    assert torch.equal(got.scale[0, keep], clean.scale[0, keep])
 
 
 @pytest.mark.parametrize("rows,cols", ROWS)
