@@ -530,6 +530,175 @@ FLCE_API int flce_process_logits(const flce_logits_problem* problem, const void*
                                  const float* bias, const void* mask, void* out, int64_t* token, float* lse,
                                  void* workspace, size_t workspace_bytes, flce_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * From one token to the next: the embedding of the ids (a table that is often
+ * the head's weight) and its gradient, the head's logits from a weight held in
+ * 4 bits, and the choice of a token from logits.  The conventions of the calls
+ * above hold.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Rows of a table by token.
+ *   tokens        N, 0 <= N <= 2^30
+ *   vocab         V, 1 <= V < 2^31 - 1
+ *   cols          1 <= D <= 2^24
+ *   weight_stride elements between the table's rows (weight: >= 0, dweight: >= cols)
+ *   out_stride    elements between out's or dout's rows (out: >= cols when tokens > 1;
+ *                 dout: >= 0, 0 reads one row N times)
+ *   padding       id whose row gets no gradient, or any number outside [0, V) for none
+ *   weight_dtype  type of weight, dweight
+ *   out_dtype     type of out, dout: weight_dtype or FLCE_F32
+ *   ids_i64       1 for int64 ids, 0 for int32 ids
+ *   accumulate    backward: 1 adds the gradient to dweight, 0 writes every row
+ *   scale         finite
+ */
+typedef struct {
+  int64_t tokens, vocab, cols;
+  int64_t weight_stride, out_stride;
+  int64_t padding;
+  int32_t weight_dtype, out_dtype;
+  int32_t ids_i64, accumulate;
+  float scale;
+  int32_t reserved;
+} flce_embedding_problem;
+
+/*
+ * out[i] = rn(weight[ids[i]] * scale), zeros where ids[i] is outside [0, V).
+ *   ids     [N]
+ *   weight  [V, D]
+ *   out     [N, D]
+ */
+FLCE_API int flce_embedding(const flce_embedding_problem* problem, const void* ids, const void* weight, void* out,
+                            flce_stream_t stream);
+
+/* Bytes of device workspace flce_embedding_backward needs (needs no GPU). */
+FLCE_API int flce_embedding_workspace_size(const flce_embedding_problem* problem, size_t* bytes);
+
+/*
+ * dweight[v] = rn(scale * sum of dout[i] over the tokens i with ids[i] = v), 0 for
+ * rows without a token; with accumulate rn(dweight[v] + ...), where rows without a
+ * token are neither read nor written.  The sums are fp32, in the tokens' order in
+ * stretches of a fixed size: the same bits from call to call.
+ *   ids      [N]; ids outside [0, V) and `padding` have no gradient
+ *   dout     [N, D]
+ *   dweight  [V, D]
+ */
+FLCE_API int flce_embedding_backward(const flce_embedding_problem* problem, const void* ids, const void* dout,
+                                     void* dweight, void* workspace, size_t workspace_bytes, flce_stream_t stream);
+
+/*
+ * Matrices in 4 bits, scaled in blocks (the MXFP4 format of the OCP Microscaling
+ * Formats specification 1.0): values of e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives), and for each 32 columns of a row a power of two.
+ *   codes   [N, 16 * ceil(D / 32)] bytes, dense: the even column's code in the low
+ *           half; the columns that fill the last block up are 0
+ *   scales  exponents + 127, in tiles of 128 rows x 4 blocks, dense, as the tensor
+ *           cores take them: [ceil(N / 128)][ceil(B / 4)][32][4][4] for B = ceil(D / 32)
+ *           blocks; row r's is at [r / 128][b / 4][r % 32][r % 128 / 32][b % 4].
+ *           Bytes of rows and blocks that the matrix does not have are 0.
+ *           255 stands for NaN.
+ *   rows    N >= 0;  cols 1 <= D <= 2^24
+ *   stride  elements between rows of x (>= 0) or out (>= cols when rows > 1)
+ *   dtype   type of x or out
+ */
+typedef struct {
+  int64_t rows, cols, stride;
+  int32_t dtype;
+  int32_t reserved;
+} flce_mxfp4_problem;
+
+/* Bytes of `codes` and `scales` (needs no GPU); dtype and stride do not matter. */
+FLCE_API int flce_mxfp4_size(const flce_mxfp4_problem* problem, size_t* codes_bytes, size_t* scales_bytes);
+
+/*
+ * x in 4 bits.  With m = max |x| over a block, its exponent is
+ * k = floor(log2(m)) - 2 within [-127, 125] (-127 for m = 0), and a code is the
+ * value nearest to x / 2^k, halves to the even code, at most 6 in size.  A block
+ * with a NaN or an infinity gets the scale NaN, and codes 0.
+ */
+FLCE_API int flce_mxfp4_quantize(const flce_mxfp4_problem* problem, const void* x, void* codes, void* scales,
+                                 flce_stream_t stream);
+
+/* out = rn(code * 2^k), in out's type. */
+FLCE_API int flce_mxfp4_dequantize(const flce_mxfp4_problem* problem, const void* codes, const void* scales, void* out,
+                                   flce_stream_t stream);
+
+/*
+ * Logits of a head whose weight is held in 4 bits:
+ *   z = logit_scale * (mx(hidden) mx(weight)^T + bias),  out = rn(cap(z))
+ * where mx() is the matrix in 4 bits: hidden is quantised in the call, as by
+ * flce_mxfp4_quantize, and cap(z) = softcap * tanh(z / softcap) for softcap > 0.
+ * The products are summed in fp32 on the tensor cores.
+ *   tokens        N >= 0;  vocab 1 <= V < 2^31 - 256;  cols 1 <= D <= 2^20
+ *   hidden_stride, out_stride  elements between rows (out: >= V when tokens > 1)
+ *   hidden_dtype, out_dtype, bias_dtype  any of the three types each
+ *   logit_scale   finite;  softcap finite, >= 0 (0: none)
+ */
+typedef struct {
+  int64_t tokens, vocab, cols;
+  int64_t hidden_stride, out_stride;
+  int32_t hidden_dtype, out_dtype, bias_dtype;
+  float logit_scale, softcap;
+  int32_t reserved;
+} flce_mxfp4_logits_problem;
+
+/* Bytes of device workspace flce_mxfp4_logits needs (needs no GPU). */
+FLCE_API int flce_mxfp4_logits_workspace_size(const flce_mxfp4_logits_problem* problem, size_t* bytes);
+
+/*
+ *   hidden  [N, D]
+ *   codes, scales  of the weight [V, D]; 16-byte aligned
+ *   bias    [V] or NULL
+ *   out     [N, V]
+ *   workspace  16-byte aligned; its first word is a device status word (see
+ *           flce_read_device_status): FLCE_ERR_TIMEOUT if the kernel gave up
+ */
+FLCE_API int flce_mxfp4_logits(const flce_mxfp4_logits_problem* problem, const void* hidden, const void* codes,
+                               const void* scales, const void* bias, void* out, void* workspace,
+                               size_t workspace_bytes, flce_stream_t stream);
+
+/*
+ * A token for each of B requests.
+ *   rows          B >= 0
+ *   vocab         V, 1 <= V <= 2^20
+ *   logits_stride elements between rows, >= 0
+ */
+typedef struct {
+  int64_t rows, vocab, logits_stride;
+  int32_t logits_dtype;
+  int32_t reserved;
+} flce_sample_problem;
+
+/*
+ * For request b: entries of -inf are left out, the others ranked by (z descending,
+ * index ascending), with weights w = exp((z - max z) / temperature[b]).
+ *   1. top-k:  the first top_k[b] ranks stay
+ *   2. top-p:  of those, the ranks before which less than top_p[b] of their whole
+ *      weight stands (the first one always)
+ *   3. min-p:  of those, the ones with w >= min_p[b]
+ *   token[b]   = the first that stays, in index order, up to which the weight of
+ *                those that stay is more than uniform[b] of their whole
+ *   logprob[b] = log of its part of that whole;  kept[b] = how many stay
+ * Weights have errors below 2^-31 of themselves and are summed exactly: the same
+ * bits from call to call, and equal logits have equal weights.
+ *   logits   [B, V]
+ *   uniform  [B] fp32 in [0, 1) (below: 0, and NaN; above: just below 1)
+ *   temperature  [B] fp32 or NULL (1).  0, below, or NaN: greedy, the lowest index of
+ *            the largest logit (logprob 0, kept 1)
+ *   top_k    [B] int64 or NULL; <= 0 or >= V: all
+ *   top_p    [B] fp32 or NULL; >= 1 or NaN: all
+ *   min_p    [B] fp32 or NULL; <= 0 or NaN: all; above 1 as 1
+ *   token    [B] int64: -1 (logprob -inf, kept 0) where every entry is -inf
+ *   logprob  [B] fp32 or NULL;  kept [B] int64 or NULL
+ * A row with a NaN gives the lowest NaN's index, logprob NaN and kept 1.  Where the
+ * largest logit is +inf, those of +inf have equal weights and the others none.
+ */
+FLCE_API int flce_sample(const flce_sample_problem* problem, const void* logits, const float* uniform,
+                         const float* temperature, const int64_t* top_k, const float* top_p, const float* min_p,
+                         int64_t* token, float* logprob, int64_t* kept, flce_stream_t stream);
+
 /* Static English description of a status code (never NULL). */
 FLCE_API const char* flce_status_string(int status);
 

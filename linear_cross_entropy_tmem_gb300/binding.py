@@ -112,6 +112,52 @@ class FlceLogitsProblem(ctypes.Structure):
     ]
 
 
+class FlceEmbeddingProblem(ctypes.Structure):
+    """Mirror of ``flce_embedding_problem``."""
+    _fields_ = [
+        ("tokens", c_int64),
+        ("vocab", c_int64),
+        ("cols", c_int64),
+        ("weight_stride", c_int64),
+        ("out_stride", c_int64),
+        ("padding", c_int64),
+        ("weight_dtype", c_int32),
+        ("out_dtype", c_int32),
+        ("ids_i64", c_int32),
+        ("accumulate", c_int32),
+        ("scale", c_float),
+        ("reserved", c_int32),
+    ]
+
+
+class FlceMxfp4Problem(ctypes.Structure):
+    """Mirror of ``flce_mxfp4_problem``."""
+    _fields_ = [("rows", c_int64), ("cols", c_int64), ("stride", c_int64), ("dtype", c_int32), ("reserved", c_int32)]
+
+
+class FlceMxfp4LogitsProblem(ctypes.Structure):
+    """Mirror of ``flce_mxfp4_logits_problem``."""
+    _fields_ = [
+        ("tokens", c_int64),
+        ("vocab", c_int64),
+        ("cols", c_int64),
+        ("hidden_stride", c_int64),
+        ("out_stride", c_int64),
+        ("hidden_dtype", c_int32),
+        ("out_dtype", c_int32),
+        ("bias_dtype", c_int32),
+        ("logit_scale", c_float),
+        ("softcap", c_float),
+        ("reserved", c_int32),
+    ]
+
+
+class FlceSampleProblem(ctypes.Structure):
+    """Mirror of ``flce_sample_problem``."""
+    _fields_ = [("rows", c_int64), ("vocab", c_int64), ("logits_stride", c_int64), ("logits_dtype", c_int32),
+                ("reserved", c_int32)]
+
+
 _LIB = None
 
 # name -> (restype, argtypes); every function ``include/*.h`` declares.
@@ -154,6 +200,15 @@ SIGNATURES = {
                                     c_size_t, c_void_p]),
     "flce_process_logits_workspace_size": (c_int, [POINTER(FlceLogitsProblem), POINTER(c_size_t)]),
     "flce_process_logits": (c_int, [POINTER(FlceLogitsProblem)] + [c_void_p] * 14 + [c_size_t, c_void_p]),
+    "flce_embedding": (c_int, [POINTER(FlceEmbeddingProblem)] + [c_void_p] * 4),
+    "flce_embedding_workspace_size": (c_int, [POINTER(FlceEmbeddingProblem), POINTER(c_size_t)]),
+    "flce_embedding_backward": (c_int, [POINTER(FlceEmbeddingProblem)] + [c_void_p] * 4 + [c_size_t, c_void_p]),
+    "flce_mxfp4_size": (c_int, [POINTER(FlceMxfp4Problem), POINTER(c_size_t), POINTER(c_size_t)]),
+    "flce_mxfp4_quantize": (c_int, [POINTER(FlceMxfp4Problem)] + [c_void_p] * 4),
+    "flce_mxfp4_dequantize": (c_int, [POINTER(FlceMxfp4Problem)] + [c_void_p] * 4),
+    "flce_mxfp4_logits_workspace_size": (c_int, [POINTER(FlceMxfp4LogitsProblem), POINTER(c_size_t)]),
+    "flce_mxfp4_logits": (c_int, [POINTER(FlceMxfp4LogitsProblem)] + [c_void_p] * 6 + [c_size_t, c_void_p]),
+    "flce_sample": (c_int, [POINTER(FlceSampleProblem)] + [c_void_p] * 10),
     "flce_read_device_status": (c_int, [c_void_p, c_void_p, POINTER(c_int)]),
     "flce_status_string": (c_char_p, [c_int]),
     "flce_abi_version": (c_int, []),

@@ -26,7 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libflce.so")
 SOURCES = ["flce_api.cu", "flce_fwd.cu", "flce_bwd.cu", "flce_noalloc.cu", "flce_norm.cu", "flce_norm_fwd.cu",
-           "flce_norm_fp8.cu", "flce_norm_fp8_left.cu", "flce_norm_bwd.cu", "flce_clip.cu", "flce_logits.cu"]
+           "flce_norm_fp8.cu", "flce_norm_fp8_left.cu", "flce_norm_bwd.cu", "flce_clip.cu", "flce_logits.cu",
+           "flce_embed.cu", "flce_mxfp4.cu", "flce_mx_logits.cu", "flce_sample.cu"]
 TORCH_SOURCE = "flce_torch.cpp"
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 

@@ -1,0 +1,615 @@
+// flce_embed.cu — embedding lookup with scaling, and the table's gradient by
+// sorted tokens: kernels and the C entry points.
+//
+//   out_i = rn(W[id_i] s),  0 where id_i is outside [0, V)
+//   dW[v] = rn(s sum of dout_i over the tokens i with id_i = v, in order)   (+ dW[v] when accumulating)
+//
+// Both are bound by memory: the lookup reads and writes a row per token, the
+// gradient reads one per token and writes the whole table.
+//
+// The gradient has three launches.  One cluster sorts the tokens by id (stable,
+// so equal ids stay in the tokens' order).  Then blocks of kChunk sorted tokens
+// sum their rows in registers; a run of one id that lies inside a chunk goes
+// straight to the table, the parts of a run that crosses a border go to fp32
+// slots.  Other blocks of the same launch write zeros to the rows that no token
+// names, so that every row is written once.  The third launch joins the parts, in
+// order.  Nothing depends on the order in which blocks run: same bits every time.
+#include <algorithm>
+#include <cmath>
+
+#include "flce_device.cuh"
+#include "flce_elem.cuh"
+#include "flce_host.h"
+
+namespace flce {
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kElems = 8;             // elements of a row that a thread holds
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+constexpr int64_t kMaxWidth = int64_t(1) << 24;
+
+__host__ __device__ constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ int64_t id_at(const void* ids, int i64, int64_t i) {
+  return i64 ? static_cast<const int64_t*>(ids)[i] : int64_t(static_cast<const int32_t*>(ids)[i]);
+}
+
+// kElems elements of a row as fp32: adjacent ones from `at` on (kVec), or one of
+// every blockDim.x from `at` on.
+template <class T>
+struct Raw {
+  Vec<T, kElems> v;
+};
+template <class T, bool kVec>
+__device__ __forceinline__ void load_elems(const T* row, int at, int cols, Raw<T>& r) {
+  if constexpr (kVec) {
+    if (at < cols) r.v = load_vec<T, kElems>(row + at);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kElems; ++e) {
+      const int c = at + e * int(blockDim.x);
+      if (c < cols) r.v.v[e] = row[c];
+    }
+  }
+}
+template <class O, bool kVec>
+__device__ __forceinline__ void store_elems(O* row, int at, int cols, const float (&x)[kElems]) {
+  if constexpr (kVec) {
+    if (at >= cols) return;
+    Vec<O, kElems> v;
+#pragma unroll
+    for (int e = 0; e < kElems; ++e) v.v[e] = from_f32<O>(x[e]);
+    store_vec<O, kElems>(row + at, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kElems; ++e) {
+      const int c = at + e * int(blockDim.x);
+      if (c < cols) row[c] = from_f32<O>(x[e]);
+    }
+  }
+}
+// A block's columns [tile * blockDim.x * kElems, ...): the thread's first one.
+template <bool kVec>
+__device__ __forceinline__ int first_col(int tile) {
+  return tile * int(blockDim.x) * kElems + int(threadIdx.x) * (kVec ? kElems : 1);
+}
+
+// ---------------------------------------------------------------------------
+// Lookup
+// ---------------------------------------------------------------------------
+struct EmbedParams {
+  const void* ids;
+  const void* weight;
+  void* out;
+  int64_t tokens, vocab, ws, os;
+  int32_t cols, tiles, ids_i64;
+  float scale;
+};
+
+// kRows tokens per block and tile of columns: their rows are under way at once.
+template <class T, class O, bool kVec, int kRows>
+__global__ void __launch_bounds__(256) embed_kernel(EmbedParams p) {
+  const int tile = int(blockIdx.x % unsigned(p.tiles));
+  const int64_t first = int64_t(blockIdx.x / unsigned(p.tiles)) * kRows;
+  const int at = first_col<kVec>(tile);
+  Raw<T> r[kRows];
+  bool there[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int64_t i = first + k;
+    const int64_t id = i < p.tokens ? id_at(p.ids, p.ids_i64, i) : -1;
+    there[k] = id >= 0 && id < p.vocab;
+    if (there[k]) load_elems<T, kVec>(static_cast<const T*>(p.weight) + id * p.ws, at, p.cols, r[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    if (first + k >= p.tokens) break;
+    float x[kElems];
+#pragma unroll
+    for (int e = 0; e < kElems; ++e) x[e] = there[k] ? __fmul_rn(to_f32(r[k].v.v[e]), p.scale) : 0.f;
+    store_elems<O, kVec>(static_cast<O*>(p.out) + (first + k) * p.os, at, p.cols, x);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Stable sort of the tokens by id
+// ---------------------------------------------------------------------------
+// (id << 32 | token), ids that have no gradient as `vocab`: they come last.
+constexpr int kSortThreads = 1024, kSortWarps = 32;
+constexpr int kMaxDigit = 10;          // bits of an id taken in one pass
+constexpr int kSortCtas = 8;           // of the cluster
+constexpr int64_t kSortOne = 4096;     // up to so many tokens one block does it: 2 us less than a cluster's barriers
+
+struct SortParams {
+  const void* ids;
+  uint64_t *a, *b;   // pass 0 writes a, pass 1 writes b, ...
+  uint32_t* joins;   // counter that the sums start from zero
+  int64_t n, vocab, padding;
+  int32_t ids_i64, passes, width;  // passes of `width` bits
+};
+
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Least significant digit first.  Every warp of the cluster owns a stretch of the
+// array: it counts its digits (32 keys at a time, equal digits found by a match
+// over the warp), the counts are summed over warps, CTAs (distributed shared
+// memory) and digits, and the warp places its keys, in order.
+__global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(SortParams p) {
+  extern __shared__ uint32_t smem[];
+  const int radix = 1 << p.width;
+  uint32_t* count = smem;                          // [warp][digit]
+  uint32_t* total = count + kSortWarps * radix;    // [digit] of this CTA
+  uint32_t* base = total + radix;                  // [digit] where this CTA's keys go
+  __shared__ uint32_t warp_sum_buf[kSortWarps];
+  griddep_release();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = int(cluster_ctarank()), ctas = int(gridDim.x);
+  const int64_t per = cdiv(cdiv(p.n, int64_t(ctas) * kSortWarps), 32) * 32;
+  const int64_t lo = min(p.n, (int64_t(rank) * kSortWarps + warp) * per), hi = min(p.n, lo + per);
+  if (rank == 0 && threadIdx.x == 0) *p.joins = 0u;
+  uint32_t* mine = count + warp * radix;
+  const uint64_t* src = nullptr;
+  uint64_t* dst = p.a;
+  auto key_at = [&](int64_t i) -> uint64_t {
+    if (src) return __ldcg(src + i);
+    const int64_t id = id_at(p.ids, p.ids_i64, i);
+    const bool counts = id >= 0 && id < p.vocab && id != p.padding;
+    return uint64_t(counts ? id : p.vocab) << 32 | uint64_t(i);
+  };
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = 32 + pass * p.width;
+    for (int d = lane; d < radix; d += 32) mine[d] = 0u;
+    __syncwarp();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+      const int64_t i = i0 + lane;
+      const bool in = i < hi;
+      const uint32_t d = in ? uint32_t(key_at(i) >> shift) & uint32_t(radix - 1) : kFull;
+      const uint32_t same = __match_any_sync(kFull, d);
+      if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    const int d = int(threadIdx.x);
+    if (d < radix) {
+      uint32_t s = 0;
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = count[w * radix + d];
+        count[w * radix + d] = s;
+        s += c;
+      }
+      total[d] = s;
+    }
+    cluster_sync();
+    uint32_t before = 0, all = 0;
+    if (d < radix) {
+      for (int c = 0; c < ctas; ++c) {
+        const uint32_t v = ld_cluster(map_to_cta(smem_u32(total + d), uint32_t(c)));
+        if (c < rank) before += v;
+        all += v;
+      }
+    }
+    // exclusive sum of `all` over the digits
+    uint32_t incl = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum_buf[warp] = incl;
+    __syncthreads();
+    uint32_t prior = lane < warp ? warp_sum_buf[lane] : 0u;
+    prior = __reduce_add_sync(kFull, prior);
+    if (d < radix) base[d] = prior + incl - all + before;
+    __syncthreads();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+      const int64_t i = i0 + lane;
+      const bool in = i < hi;
+      const uint64_t key = in ? key_at(i) : 0ull;
+      const uint32_t g = in ? uint32_t(key >> shift) & uint32_t(radix - 1) : kFull;
+      const uint32_t same = __match_any_sync(kFull, g);
+      if (in) dst[base[g] + mine[g] + __popc(same & ((1u << lane) - 1u))] = key;
+      __syncwarp();
+      if (in && lane == __ffs(same) - 1) mine[g] += __popc(same);
+      __syncwarp();
+    }
+    cluster_sync();  // the keys are there, and nobody reads `total` any more
+    src = dst;
+    dst = dst == p.a ? p.b : p.a;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sums over the sorted tokens
+// ---------------------------------------------------------------------------
+constexpr int kChunk = 32;             // sorted tokens of a block: a warp's worth of keys
+constexpr int kAhead = 4;              // rows under way at once
+constexpr int kZeroBytes = 128 << 10;  // of the table that a block clears
+constexpr int kZeroRows = 4096;        // at most
+
+struct EmbedBwdParams {
+  const uint64_t* sorted;
+  const void* dout;
+  void* dweight;
+  float* part;        // [chunk][2][cols]: the run that enters a chunk, the run that leaves it
+  uint32_t* joins;    // number of runs that cross a border, then the chunks in which they begin
+  int64_t n, vocab, ds, ws;
+  int32_t cols, tiles, chunks, zero_rows;
+  float scale;
+  int32_t accumulate;
+};
+
+__device__ __forceinline__ uint32_t key_of(uint64_t e) { return uint32_t(e >> 32); }
+
+// First place in the sorted tokens [lo, hi) whose id is at least `id`; whole warps, 32 probes at a time.
+__device__ __forceinline__ int64_t lower_bound(const uint64_t* sorted, int64_t lo, int64_t hi, uint32_t id) {
+  while (hi > lo) {
+    const int64_t step = cdiv(hi - lo, 32), i = lo + int64_t(threadIdx.x & 31) * step;
+    const int c = __popc(__ballot_sync(kFull, i < hi && key_of(sorted[i]) < id));
+    if (step == 1 || c == 0) return lo + c;
+    const int64_t first = lo;
+    lo = first + int64_t(c - 1) * step + 1;
+    hi = min(hi, first + int64_t(c) * step);
+  }
+  return lo;
+}
+
+template <class O, bool kVec>
+__device__ __forceinline__ void write_row(const EmbedBwdParams& p, uint32_t id, int at, const float (&acc)[kElems]) {
+  O* row = static_cast<O*>(p.dweight) + int64_t(id) * p.ws;
+  float x[kElems];
+#pragma unroll
+  for (int e = 0; e < kElems; ++e) x[e] = __fmul_rn(acc[e], p.scale);
+  if (p.accumulate) {
+    Raw<O> old;
+    load_elems<O, kVec>(row, at, p.cols, old);
+#pragma unroll
+    for (int e = 0; e < kElems; ++e) x[e] = __fadd_rn(to_f32(old.v.v[e]), x[e]);
+  }
+  store_elems<O, kVec>(row, at, p.cols, x);
+}
+
+// Zeros to the rows [r0, r1) that no token names.
+template <class O>
+__device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, int64_t r0, int64_t r1, uint32_t* named) {
+  const int rows = int(r1 - r0), warps = int(blockDim.x >> 5), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < (rows + 31) / 32; i += blockDim.x) named[i] = 0u;
+  const int64_t lo = lower_bound(p.sorted, 0, p.n, uint32_t(r0)), hi = lower_bound(p.sorted, lo, p.n, uint32_t(r1));
+  __syncthreads();
+  if (hi - lo <= int64_t(rows) * 16) {
+    for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) {
+      const int r = int(key_of(p.sorted[i]) - uint32_t(r0));
+      atomicOr(&named[r >> 5], 1u << (r & 31));
+    }
+  } else {  // long runs: look for the rows instead
+    for (int r = warp; r < rows; r += warps) {
+      const int64_t i = lower_bound(p.sorted, lo, hi, uint32_t(r0 + r));
+      if (lane == 0 && i < hi && key_of(p.sorted[i]) == uint32_t(r0 + r)) atomicOr(&named[r >> 5], 1u << (r & 31));
+    }
+  }
+  __syncthreads();
+  // a warp per row: single elements up to a 16-byte boundary, whole vectors, the rest
+  constexpr int kV = 16 / sizeof(O);
+  const O zero = from_f32<O>(0.f);
+  for (int r = warp; r < rows; r += warps) {
+    if ((named[r >> 5] >> (r & 31)) & 1u) continue;
+    O* row = static_cast<O*>(p.dweight) + (r0 + r) * p.ws;
+    const int head = min(p.cols, int((kV - (reinterpret_cast<uintptr_t>(row) / sizeof(O)) % kV) % kV));
+    const int vecs = (p.cols - head) / kV, tail = head + vecs * kV;
+    if (lane < head) row[lane] = zero;
+    for (int i = lane; i < vecs; i += 32) *reinterpret_cast<uint4*>(row + head + i * kV) = make_uint4(0u, 0u, 0u, 0u);
+    if (tail + lane < p.cols) row[tail + lane] = zero;
+  }
+}
+
+template <class T, class O, bool kVec>
+__global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdParams p) {
+  __shared__ uint32_t named[kZeroRows / 32];
+  __shared__ uint32_t keys[kChunk + 2];
+  __shared__ uint32_t tokens[kChunk];
+  griddep_wait();  // the tokens are sorted
+  griddep_release();
+  const int64_t sums = int64_t(p.chunks) * p.tiles;
+  if (int64_t(blockIdx.x) >= sums) {
+    const int64_t r0 = (int64_t(blockIdx.x) - sums) * p.zero_rows;
+    clear_rows<O>(p, r0, min(p.vocab, r0 + p.zero_rows), named);
+    return;
+  }
+  const int tile = int(blockIdx.x % unsigned(p.tiles));
+  const int chunk = int(blockIdx.x / unsigned(p.tiles));
+  const int64_t begin = int64_t(chunk) * kChunk;
+  const int len = int(min(int64_t(kChunk), p.n - begin));
+  const int at = first_col<kVec>(tile);
+  // keys[1 + j] is the chunk's j-th; before and after it, those of its neighbours
+  if (threadIdx.x < kChunk) {
+    const int j = int(threadIdx.x);
+    const uint64_t e = j < len ? p.sorted[begin + j] : ~0ull;
+    keys[1 + j] = key_of(e);
+    tokens[j] = uint32_t(e);
+    if (j == 0) keys[0] = begin > 0 ? key_of(p.sorted[begin - 1]) : kFull;
+    if (j == 1) keys[kChunk + 1] = begin + kChunk < p.n ? key_of(p.sorted[begin + kChunk]) : kFull;
+  }
+  __syncthreads();
+  const uint32_t none = uint32_t(p.vocab);  // the key of tokens without a gradient
+  const bool enters = keys[0] == keys[1];
+  float* part = p.part + int64_t(chunk) * 2 * p.cols;
+  float acc[kElems];
+#pragma unroll
+  for (int e = 0; e < kElems; ++e) acc[e] = 0.f;
+  bool inside = false;  // the current run began in this chunk
+  for (int j0 = 0; j0 < len; j0 += kAhead) {
+    if (keys[1 + j0] == none) break;
+    Raw<T> r[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (j0 + u < len && keys[1 + j0 + u] != none)
+        load_elems<T, kVec>(static_cast<const T*>(p.dout) + int64_t(tokens[j0 + u]) * p.ds, at, p.cols, r[u]);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int j = j0 + u;
+      const uint32_t key = keys[1 + j];
+      if (j >= len || key == none) break;
+      if (j == 0 ? !enters : key != keys[j]) inside = true;
+#pragma unroll
+      for (int e = 0; e < kElems; ++e) acc[e] += to_f32(r[u].v.v[e]);
+      if (keys[2 + j] == key && j + 1 < len) continue;
+      // the run ends here, or the chunk does
+      const bool leaves = keys[2 + j] == key;
+      if (!inside || leaves) {
+        store_elems<float, kVec>(part + (inside ? p.cols : 0), at, p.cols, acc);
+        if (inside && tile == 0 && threadIdx.x == 0) p.joins[1 + atomicAdd(p.joins, 1u)] = uint32_t(chunk);
+      } else {
+        write_row<O, kVec>(p, key, at, acc);
+      }
+#pragma unroll
+      for (int e = 0; e < kElems; ++e) acc[e] = 0.f;
+    }
+  }
+}
+
+// Runs that cross a border: the part of the chunk in which the run begins and
+// those of the chunks that it enters.  kJoinWarps warps take every kJoinWarps-th
+// part each, for 32 columns; their sums are added in order.
+constexpr int kJoinWarps = 8;
+template <class O>
+__global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(EmbedBwdParams p) {
+  __shared__ float buf[kJoinWarps][32];
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tiles = (p.cols + 31) / 32;
+  const int64_t work = int64_t(*p.joins) * tiles;
+  for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
+    const int chunk = int(p.joins[1 + w / tiles]);
+    const int c = int(w % tiles) * 32 + lane;
+    const int64_t last = min(p.n, (int64_t(chunk) + 1) * kChunk) - 1;
+    const uint32_t id = key_of(p.sorted[last]);
+    const int64_t end = lower_bound(p.sorted, last, p.n, id + 1);  // one past the run
+    const int parts = int((end - 1) / kChunk) - chunk + 1;
+    float s = 0.f;
+    if (c < p.cols) {
+#pragma unroll 4
+      for (int i = warp; i < parts; i += kJoinWarps)
+        s += p.part[(int64_t(chunk + i) * 2 + (i == 0)) * p.cols + c];
+    }
+    buf[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < p.cols) {
+#pragma unroll
+      for (int i = 1; i < kJoinWarps; ++i) s += buf[i][lane];
+      O* to = static_cast<O*>(p.dweight) + int64_t(id) * p.ws + c;
+      s = __fmul_rn(s, p.scale);
+      *to = from_f32<O>(p.accumulate ? __fadd_rn(to_f32(*to), s) : s);
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+int validate(const flce_embedding_problem* p) {
+  if (!p) return FLCE_ERR_INVALID_ARG;
+  if (p->tokens < 0 || p->tokens > kMaxTokens || p->vocab < 1 || p->vocab >= INT32_MAX || p->cols < 1 ||
+      p->cols > kMaxWidth || p->weight_stride < 0 || p->out_stride < 0)
+    return FLCE_ERR_INVALID_ARG;
+  if (!known_dtype(p->weight_dtype) || !known_dtype(p->out_dtype)) return FLCE_ERR_UNSUPPORTED_DTYPE;
+  if (p->out_dtype != p->weight_dtype && p->out_dtype != FLCE_F32) return FLCE_ERR_DTYPE_MISMATCH;
+  if (!std::isfinite(p->scale)) return FLCE_ERR_INVALID_ARG;
+  return FLCE_OK;
+}
+
+// Threads of a block whose threads hold kElems columns each.
+int row_threads(int64_t cols) { return int(std::min<int64_t>(256, cdiv(cdiv(cols, kElems), 32) * 32)); }
+
+// Whether all rows start on a boundary of kElems elements, so that vectors do.
+bool whole_vectors(int64_t cols, const void* p, int64_t stride, const void* q, int64_t stride2) {
+  return cols % kElems == 0 && aligned_to(p, 16) && aligned_to(q, 16) && stride % kElems == 0 && stride2 % kElems == 0;
+}
+
+struct BwdLayout {
+  size_t a, b, joins, part, bytes;
+};
+BwdLayout bwd_layout(const flce_embedding_problem* p) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t n = size_t(p->tokens), chunks = size_t(cdiv(p->tokens, kChunk));
+  BwdLayout l;
+  l.a = 0;
+  l.b = up(n * 8);
+  l.joins = l.b + up(n * 8);
+  l.part = l.joins + up((chunks + 1) * 4);
+  l.bytes = l.part + up(chunks * 2 * size_t(p->cols) * 4);
+  return l;
+}
+
+template <class T, class O, bool kVec>
+cudaError_t launch_embed(EmbedParams& q, cudaStream_t st) {
+  const int threads = row_threads(q.cols);
+  q.tiles = int32_t(cdiv(q.cols, int64_t(threads) * kElems));
+  // four rows at once where that leaves enough blocks for every SM
+  if (cdiv(q.tokens, 4) * q.tiles >= 1024) {
+    embed_kernel<T, O, kVec, 4><<<unsigned(cdiv(q.tokens, 4) * q.tiles), threads, 0, st>>>(q);
+  } else {
+    embed_kernel<T, O, kVec, 1><<<unsigned(q.tokens * q.tiles), threads, 0, st>>>(q);
+  }
+  return cudaGetLastError();
+}
+template <class T, class O>
+cudaError_t launch_embed(EmbedParams& q, cudaStream_t st) {
+  return whole_vectors(q.cols, q.weight, q.ws, q.out, q.os) ? launch_embed<T, O, true>(q, st)
+                                                            : launch_embed<T, O, false>(q, st);
+}
+
+cudaError_t launch_sort(const SortParams& s, cudaStream_t st) {
+  const int radix = 1 << s.width;
+  const size_t smem = size_t(kSortWarps + 2) * radix * 4;
+  cudaError_t e = cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (kSortWarps + 2) * (1 << kMaxDigit) * 4);
+  if (e != cudaSuccess) return e;
+  const unsigned ctas = s.n <= kSortOne ? 1 : kSortCtas;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sort_tokens_kernel, s);
+}
+
+template <class T, class O, bool kVec>
+cudaError_t launch_sum(EmbedBwdParams& q, cudaStream_t st) {
+  const int threads = row_threads(q.cols);
+  q.tiles = int32_t(cdiv(q.cols, int64_t(threads) * kElems));
+  const int64_t clear = q.accumulate ? 0 : cdiv(q.vocab, q.zero_rows);
+  return launch_dependent(embed_sum_kernel<T, O, kVec>, unsigned(int64_t(q.chunks) * q.tiles + clear), threads, st, q);
+}
+template <class T, class O>
+cudaError_t launch_sum(EmbedBwdParams& q, cudaStream_t st) {
+  return whole_vectors(q.cols, q.dout, q.ds, q.dweight, q.ws) ? launch_sum<T, O, true>(q, st)
+                                                              : launch_sum<T, O, false>(q, st);
+}
+
+}  // namespace
+}  // namespace flce
+
+using namespace flce;
+
+extern "C" {
+
+int flce_embedding(const flce_embedding_problem* problem, const void* ids, const void* weight, void* out,
+                   flce_stream_t stream) {
+  const flce_embedding_problem* p = problem;
+  FLCE_TRY(validate(p));
+  if (p->tokens == 0) return FLCE_OK;
+  if (!ids || !weight || !out || (p->tokens > 1 && p->out_stride < p->cols)) return FLCE_ERR_INVALID_ARG;
+  if (!aligned_to(ids, p->ids_i64 ? 8 : 4) || !aligned_to(weight, elem_size(p->weight_dtype)) ||
+      !aligned_to(out, elem_size(p->out_dtype)))
+    return FLCE_ERR_MISALIGNED;
+  if (p->tokens * cdiv(p->cols, 32 * kElems) > INT32_MAX) return FLCE_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  FLCE_TRY(get_device(&dev));
+  FLCE_TRY(check_local(dev, ids, weight, out));
+  EmbedParams q{};
+  q.ids = ids;
+  q.weight = weight;
+  q.out = out;
+  q.tokens = p->tokens;
+  q.vocab = p->vocab;
+  q.ws = p->weight_stride;
+  q.os = p->out_stride;
+  q.cols = int32_t(p->cols);
+  q.ids_i64 = p->ids_i64;
+  q.scale = p->scale;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return logged(FLCE_LAUNCH_OTHER, st, [&] {
+    if (p->weight_dtype == FLCE_F32) return launch_embed<float, float>(q, st);
+    if (p->weight_dtype == FLCE_BF16)
+      return p->out_dtype == FLCE_F32 ? launch_embed<__nv_bfloat16, float>(q, st)
+                                      : launch_embed<__nv_bfloat16, __nv_bfloat16>(q, st);
+    return p->out_dtype == FLCE_F32 ? launch_embed<__half, float>(q, st) : launch_embed<__half, __half>(q, st);
+  });
+}
+
+int flce_embedding_workspace_size(const flce_embedding_problem* problem, size_t* bytes) {
+  if (!bytes) return FLCE_ERR_INVALID_ARG;
+  FLCE_TRY(validate(problem));
+  *bytes = bwd_layout(problem).bytes + 256;
+  return FLCE_OK;
+}
+
+int flce_embedding_backward(const flce_embedding_problem* problem, const void* ids, const void* dout, void* dweight,
+                            void* workspace, size_t workspace_bytes, flce_stream_t stream) {
+  const flce_embedding_problem* p = problem;
+  size_t need = 0;
+  FLCE_TRY(flce_embedding_workspace_size(p, &need));
+  if (p->weight_stride < p->cols && p->vocab > 1) return FLCE_ERR_INVALID_ARG;
+  if (p->tokens == 0 && p->accumulate) return FLCE_OK;
+  if ((p->tokens > 0 && (!ids || !dout)) || !dweight || !workspace) return FLCE_ERR_INVALID_ARG;
+  if (!aligned_to(ids, p->ids_i64 ? 8 : 4) || !aligned_to(dout, elem_size(p->out_dtype)) ||
+      !aligned_to(dweight, elem_size(p->weight_dtype)) || !aligned_to(workspace, 16))
+    return FLCE_ERR_MISALIGNED;
+  if (workspace_bytes < need) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  if (cdiv(p->tokens, kChunk) * cdiv(p->cols, 32 * kElems) + p->vocab > INT32_MAX) return FLCE_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  FLCE_TRY(get_device(&dev));
+  FLCE_TRY(check_local(dev, ids, dout, dweight, workspace));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const BwdLayout l = bwd_layout(p);
+  SortParams s{};
+  s.ids = ids;
+  s.a = reinterpret_cast<uint64_t*>(ws + l.a);
+  s.b = reinterpret_cast<uint64_t*>(ws + l.b);
+  s.joins = reinterpret_cast<uint32_t*>(ws + l.joins);
+  s.n = p->tokens;
+  s.vocab = p->vocab;
+  s.padding = p->padding;
+  s.ids_i64 = p->ids_i64;
+  int bits = 1;  // of the largest key, vocab
+  while ((p->vocab >> bits) != 0) ++bits;
+  s.passes = int32_t(cdiv(bits, kMaxDigit));
+  s.width = int32_t(cdiv(bits, s.passes));
+  FLCE_TRY(logged(FLCE_LAUNCH_OTHER, st, [&] { return launch_sort(s, st); }));
+  EmbedBwdParams q{};
+  q.sorted = s.passes % 2 ? s.a : s.b;
+  q.dout = dout;
+  q.dweight = dweight;
+  q.part = reinterpret_cast<float*>(ws + l.part);
+  q.joins = s.joins;
+  q.n = p->tokens;
+  q.vocab = p->vocab;
+  q.ds = p->out_stride;
+  q.ws = p->weight_stride;
+  q.cols = int32_t(p->cols);
+  q.chunks = int32_t(cdiv(p->tokens, kChunk));
+  q.zero_rows = int32_t(std::max<int64_t>(1, std::min<int64_t>(kZeroRows, kZeroBytes / (p->cols * elem_size(p->weight_dtype)))));
+  q.scale = p->scale;
+  q.accumulate = p->accumulate;
+  FLCE_TRY(logged(FLCE_LAUNCH_OTHER, st, [&] {
+    if (p->weight_dtype == FLCE_F32) return launch_sum<float, float>(q, st);
+    if (p->weight_dtype == FLCE_BF16)
+      return p->out_dtype == FLCE_F32 ? launch_sum<float, __nv_bfloat16>(q, st)
+                                      : launch_sum<__nv_bfloat16, __nv_bfloat16>(q, st);
+    return p->out_dtype == FLCE_F32 ? launch_sum<float, __half>(q, st) : launch_sum<__half, __half>(q, st);
+  }));
+  if (q.chunks < 2) return FLCE_OK;  // no border to cross
+  const unsigned grid = unsigned(std::min<int64_t>(int64_t(q.chunks) * cdiv(q.cols, 32), int64_t(dev.num_sms) * 8));
+  return logged(FLCE_LAUNCH_OTHER, st, [&] {
+    if (p->weight_dtype == FLCE_F32) return launch_dependent(embed_join_kernel<float>, grid, kJoinWarps * 32, st, q);
+    if (p->weight_dtype == FLCE_BF16)
+      return launch_dependent(embed_join_kernel<__nv_bfloat16>, grid, kJoinWarps * 32, st, q);
+    return launch_dependent(embed_join_kernel<__half>, grid, kJoinWarps * 32, st, q);
+  });
+}
+
+}  // extern "C"

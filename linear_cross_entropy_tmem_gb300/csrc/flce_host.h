@@ -3,6 +3,7 @@
 // flce_api.cu.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -43,6 +44,11 @@ struct LocalRanges {
   uintptr_t begin = 0, end = 0;  // the last allocation found local
 };
 int check_local(const DeviceInfo& dev, const void* p, LocalRanges* known);
+
+// 2-D map of bytes with the 128-byte swizzle (rows `row_bytes` apart, boxes of
+// box_inner bytes x box_outer rows); what lies outside reads as 0.
+int make_byte_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_inner,
+                  uint32_t box_outer);
 
 int log_begin(cudaStream_t st, flce_launch_record** rec);
 int log_end(int kind, cudaStream_t st, flce_launch_record* rec);
