@@ -245,7 +245,9 @@ def load(path: str = LIB_PATH):
 # What flce_torch calls, in the order of its table.
 _MARSHALLED = ("flce_add_rms_norm", "flce_add_rms_norm_fp8", "flce_add_rms_norm_workspace_size",
                "flce_add_rms_norm_backward", "flce_grad_norm_workspace_size", "flce_grad_norm", "flce_clip_grad_norm",
-               "flce_process_logits_workspace_size", "flce_process_logits")
+               "flce_process_logits_workspace_size", "flce_process_logits", "flce_embedding",
+               "flce_embedding_workspace_size", "flce_embedding_backward", "flce_mxfp4_quantize",
+               "flce_mxfp4_dequantize", "flce_mxfp4_logits_workspace_size", "flce_mxfp4_logits", "flce_sample")
 _TORCH = None
 
 

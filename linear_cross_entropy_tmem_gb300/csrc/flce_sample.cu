@@ -17,7 +17,7 @@
 // their order, and equal logits have equal weights.
 //
 // Top-k and top-p cut the ranking at one place.  A first histogram, over the distance
-// from the maximum in steps of 2^(1/128) of the weight, names the bins in which
+// from the maximum in steps of 2^(1/64) of the weight, names the bins in which
 // it lies.  If few entries stand up to there, one CTA lists, sorts and
 // finishes them.  Else the entries of those bins are listed and sorted, or, where
 // they are many (ties), found by histograms over ever smaller intervals of (value,
@@ -41,7 +41,7 @@ constexpr int kThreadsS = 1024;
 constexpr int kWarpsS = kThreadsS / 32;
 constexpr int kMaxCtas = 16;           // of a cluster
 constexpr int kBins = 2048;
-constexpr float kBinsPerOctave = 128.f; // of the first histogram: 16 octaves below the largest weight
+constexpr float kBinsPerOctave = 64.f; // of the first histogram: 32 octaves below the largest weight
 constexpr uint32_t kList = kThreadsS;  // entries that one block finishes, one per thread
 constexpr int64_t kMaxVocab = 1 << 20; // a CTA's limb sums (65536 entries of 16 bits) fit 32 bits
 
@@ -888,12 +888,12 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
     }
     if (r.nucleus) {
       // Estimates of the mass up to each bin name the bins in which it reaches p of the whole.  A
-      // bin's weights lie within 2^(1/256) = 1 + 0.0027 of its middle's, and errors before and
-      // behind the border count 1 - p and p in their difference: at most 0.0054 p (1 - p) of the
+      // bin's weights lie within 2^(1/128) = 1 + 0.0054 of its middle's, and errors before and
+      // behind the border count 1 - p and p in their difference: at most 0.0109 p (1 - p) of the
       // whole.  (That it is reached there is seen below, from exact sums.)
       const uint64_t e_mine = e_upto;
       const float e_whole = float(block_scan(s, e_upto, none).a), goal = r.top_p * e_whole;
-      const float slack = e_whole * (0.0056f * fmaxf(r.top_p * (1.f - r.top_p), 0.f) + 2e-6f);
+      const float slack = e_whole * (0.0112f * fmaxf(r.top_p * (1.f - r.top_p), 0.f) + 2e-6f);
       float e_at = float(e_upto - e_mine);
       if (threadIdx.x < 2) s.at[threadIdx.x] = kBins - 1;
       __syncthreads();

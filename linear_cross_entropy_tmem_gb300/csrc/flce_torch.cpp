@@ -1,13 +1,13 @@
 // flce_torch.cpp — native marshalling of torch tensors for the operators on
-// either side of the head (Python module flce_torch).
+// either side of the head and from one token to the next (Python module flce_torch).
 //
 // A decoding step's call does a few microseconds of GPU work, and a list of a
 // hundred gradients little more; reading the tensors' fields from Python took
 // 20 to 250 microseconds.  These functions read them here, allocate the outputs
 // and call the C entry points.  They take the calls whose tensors are as the
 // entry points want them (CUDA, one device, known types, matching shapes, rows
-// of adjacent elements) and return None for any other, which head_ops.py then
-// views, copies or refuses with its own message.  Otherwise they return the
+// of adjacent elements) and return None for any other, which head_ops.py or
+// token_ops.py then views, copies or refuses with its own message.  Otherwise they return the
 // outputs as a tuple, or an int: the status of a call that failed.
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
@@ -34,6 +34,14 @@ struct Entry {
   decltype(&flce_clip_grad_norm) clip;
   decltype(&flce_process_logits_workspace_size) logits_ws;
   decltype(&flce_process_logits) logits;
+  decltype(&flce_embedding) embedding;
+  decltype(&flce_embedding_workspace_size) embedding_ws;
+  decltype(&flce_embedding_backward) embedding_bwd;
+  decltype(&flce_mxfp4_quantize) mx_quantize;
+  decltype(&flce_mxfp4_dequantize) mx_dequantize;
+  decltype(&flce_mxfp4_logits_workspace_size) mx_logits_ws;
+  decltype(&flce_mxfp4_logits) mx_logits;
+  decltype(&flce_sample) sample;
 } g_entry;
 constexpr Py_ssize_t kEntries = sizeof(Entry) / sizeof(void*);
 
@@ -56,6 +64,9 @@ PyObject* status(int rc) { return PyLong_FromLong(rc); }
 int code_of(at::ScalarType t) {
   return t == at::kFloat ? FLCE_F32 : t == at::kBFloat16 ? FLCE_BF16 : t == at::kHalf ? FLCE_F16 : -1;
 }
+
+// FLCE_* type to torch's.
+constexpr at::ScalarType kTypes[] = {at::kFloat, at::kBFloat16, at::kHalf};
 
 // An argument: a tensor of the call's device, or none.
 struct Arg {
@@ -355,7 +366,6 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int oc = code_of(out.scalar_type());
     if (out.sizes() != z->sizes() || oc < 0 || (want >= 0 && oc != want) || (v > 1 && out.stride(1) != 1)) Py_RETURN_NONE;
   } else {
-    static const at::ScalarType kTypes[] = {at::kFloat, at::kBFloat16, at::kHalf};
     out = empty({b, v}, want < 0 ? z->scalar_type() : kTypes[want], *z.t);
   }
   p.out_stride = out.stride(0);
@@ -385,10 +395,220 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+bool ids_of(const Arg& a) {
+  return (a->scalar_type() == at::kLong || a->scalar_type() == at::kInt) && a->is_contiguous();
+}
+
+// (weight, ids, scale, out type or -1) -> (out,)
+PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 4) return PyErr_Format(PyExc_TypeError, "embedding takes 4 arguments");
+  const Arg w = arg(a[0]);
+  if (!w || !w.ok || w->dim() != 2 || w->size(0) < 1) Py_RETURN_NONE;
+  const Arg ids = arg(a[1], w->get_device());
+  const Rows rows(*w.t);
+  const int code = code_of(w->scalar_type());
+  if (!ids || !ids.ok || !ids_of(ids) || !rows.ok || code < 0) Py_RETURN_NONE;
+  const double scale = PyFloat_AsDouble(a[2]);
+  const long want = PyLong_AsLong(a[3]);
+  if (PyErr_Occurred()) return nullptr;
+  std::vector<int64_t> size = ids->sizes().vec();
+  size.push_back(rows.d);
+  const Tensor out = empty(size, want < 0 ? w->scalar_type() : kTypes[want], *w.t);
+  const flce_embedding_problem p = {ids->numel(), rows.n, rows.d, rows.stride, rows.d, -1, code,
+                                    want < 0 ? code : int32_t(want), ids->scalar_type() == at::kLong, 0, float(scale), 0};
+  const int rc = g_entry.embedding(&p, ids.ptr(), w.ptr(), out.numel() ? out.data_ptr() : nullptr, stream_of(*w.t));
+  if (rc != FLCE_OK) return status(rc);
+  return pack({out});
+  END_HANDLE_TH_ERRORS
+}
+
+// (dout, ids, vocab, scale, padding, type or -1, dweight or None, workspace) -> (dweight,)
+PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 8) return PyErr_Format(PyExc_TypeError, "embedding_backward takes 8 arguments");
+  const Arg d = arg(a[0]);
+  if (!d || !d.ok || d->dim() < 1) Py_RETURN_NONE;
+  const Arg ids = arg(a[1], d->get_device()), given = arg(a[6], d->get_device());
+  const Rows rows(*d.t);
+  const int code = code_of(d->scalar_type());
+  if (!ids || !ids.ok || !ids_of(ids) || !given.ok || !rows.ok || code < 0) Py_RETURN_NONE;
+  if (ids->sizes() != d->sizes().slice(0, d->dim() - 1)) Py_RETURN_NONE;
+  const int64_t vocab = PyLong_AsLongLong(a[2]), padding = PyLong_AsLongLong(a[4]);
+  const double scale = PyFloat_AsDouble(a[3]);
+  const long want = PyLong_AsLong(a[5]);
+  if (PyErr_Occurred()) return nullptr;
+  if (vocab < 1 || vocab >= INT32_MAX) Py_RETURN_NONE;
+  Tensor dw;
+  if (given) {
+    dw = *given.t;
+    if (dw.dim() != 2 || dw.size(0) != vocab || dw.size(1) != rows.d || (rows.d > 1 && dw.stride(1) != 1) ||
+        code_of(dw.scalar_type()) < 0 || (want >= 0 && code_of(dw.scalar_type()) != want))
+      Py_RETURN_NONE;
+  } else {
+    dw = empty({vocab, rows.d}, want < 0 ? d->scalar_type() : kTypes[want], *d.t);
+  }
+  const flce_embedding_problem p = {rows.n, vocab, rows.d, dw.stride(0), rows.stride, padding,
+                                    code_of(dw.scalar_type()), code, ids->scalar_type() == at::kLong, bool(given),
+                                    float(scale), 0};
+  size_t bytes = 0;
+  int rc = g_entry.embedding_ws(&p, &bytes);
+  if (rc != FLCE_OK) return status(rc);
+  Tensor ws;
+  if (!workspace(a[7], bytes, *d.t, &ws)) Py_RETURN_NONE;
+  rc = g_entry.embedding_bwd(&p, ids.ptr(), d.ptr(), dw.data_ptr(), ws.data_ptr(), bytes, stream_of(*d.t));
+  if (rc != FLCE_OK) return status(rc);
+  if (given) wrote(dw);
+  PyObject* r = pack({dw});
+  if (r && given) {  // the caller's own object
+    Py_INCREF(a[6]);
+    PyTuple_SetItem(r, 0, a[6]);
+  }
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
+// A matrix in 4 bits: contiguous codes and scales of the sizes that its columns ask for.
+struct Mx {
+  Arg codes, scales;
+  int64_t n = 0, d = 0;
+  bool ok = false;
+  Mx(PyObject* c, PyObject* s, PyObject* cols, int64_t device) : codes(arg(c, device)) {
+    d = PyLong_AsLongLong(cols);
+    if (!codes || !codes.ok || codes->dim() != 2 || d < 1 || d > (1 << 24)) return;
+    scales = arg(s, codes->get_device());
+    n = codes->size(0);
+    const int64_t blocks = (d + 31) / 32;
+    ok = scales && scales.ok && codes->size(1) == blocks * 16 && scales->dim() == 5 &&
+         scales->size(0) == (n + 127) / 128 && scales->size(1) == (blocks + 3) / 4 && scales->size(2) == 32 &&
+         scales->size(3) == 4 && scales->size(4) == 4 && codes->scalar_type() == at::kByte &&
+         scales->scalar_type() == at::kByte && codes->is_contiguous() && scales->is_contiguous();
+  }
+};
+
+// (x,) -> (codes, scales)
+PyObject* mxfp4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 1) return PyErr_Format(PyExc_TypeError, "mxfp4_quantize takes 1 argument");
+  const Arg x = arg(a[0]);
+  if (!x || !x.ok) Py_RETURN_NONE;
+  const Rows rows(*x.t);
+  const int code = code_of(x->scalar_type());
+  if (!rows.ok || code < 0) Py_RETURN_NONE;
+  const int64_t blocks = (rows.d + 31) / 32;
+  const Tensor codes = empty({rows.n, blocks * 16}, at::kByte, *x.t);
+  const Tensor scales = empty({(rows.n + 127) / 128, (blocks + 3) / 4, 32, 4, 4}, at::kByte, *x.t);
+  const flce_mxfp4_problem p = {rows.n, rows.d, rows.stride, code, 0};
+  const bool any = rows.n > 0;
+  const int rc = g_entry.mx_quantize(&p, x.ptr(), any ? codes.data_ptr() : nullptr, any ? scales.data_ptr() : nullptr,
+                                     stream_of(*x.t));
+  if (rc != FLCE_OK) return status(rc);
+  return pack({codes, scales});
+  END_HANDLE_TH_ERRORS
+}
+
+// (codes, scales, cols, out type) -> (out,)
+PyObject* mxfp4_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 4) return PyErr_Format(PyExc_TypeError, "mxfp4_dequantize takes 4 arguments");
+  const Mx q(a[0], a[1], a[2], -1);
+  const long want = PyLong_AsLong(a[3]);
+  if (PyErr_Occurred()) return nullptr;
+  if (!q.ok) Py_RETURN_NONE;
+  const Tensor out = empty({q.n, q.d}, kTypes[want], *q.codes.t);
+  const flce_mxfp4_problem p = {q.n, q.d, q.d, int32_t(want), 0};
+  const int rc = g_entry.mx_dequantize(&p, q.codes.ptr(), q.scales.ptr(), out.numel() ? out.data_ptr() : nullptr,
+                                       stream_of(out));
+  if (rc != FLCE_OK) return status(rc);
+  return pack({out});
+  END_HANDLE_TH_ERRORS
+}
+
+// (hidden, codes, scales, cols, bias, logit_scale, softcap, out type or -1, out, workspace) -> (out,)
+PyObject* mxfp4_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 10) return PyErr_Format(PyExc_TypeError, "mxfp4_logits takes 10 arguments");
+  const Arg h = arg(a[0]);
+  if (!h || !h.ok || h->dim() < 1) Py_RETURN_NONE;
+  const int64_t dev = h->get_device();
+  const Mx w(a[1], a[2], a[3], dev);
+  const Arg bias = arg(a[4], dev), given = arg(a[8], dev);
+  const Rows rows(*h.t);
+  const int code = code_of(h->scalar_type()), bcode = bias ? code_of(bias->scalar_type()) : FLCE_F32;
+  const double scale = PyFloat_AsDouble(a[5]), cap = PyFloat_AsDouble(a[6]);
+  const long want = PyLong_AsLong(a[7]);
+  if (PyErr_Occurred()) return nullptr;
+  if (!w.ok || !bias.ok || !given.ok || !rows.ok || rows.d != w.d || w.n < 1 || code < 0 || bcode < 0) Py_RETURN_NONE;
+  if (bias && !vector_of(bias, w.n, bias->scalar_type())) Py_RETURN_NONE;
+  std::vector<int64_t> size = h->sizes().vec();
+  size.back() = w.n;
+  Tensor out;
+  int64_t stride = w.n;
+  if (given) {
+    out = *given.t;
+    const Rows o(out);
+    if (!o.ok || out.sizes() != at::IntArrayRef(size) || code_of(out.scalar_type()) < 0 ||
+        (want >= 0 && code_of(out.scalar_type()) != want))
+      Py_RETURN_NONE;
+    stride = o.stride;
+  } else {
+    out = empty(size, want < 0 ? h->scalar_type() : kTypes[want], *h.t);
+  }
+  const flce_mxfp4_logits_problem p = {rows.n, w.n, w.d, rows.stride, stride, code, code_of(out.scalar_type()), bcode,
+                                       float(scale), float(cap), 0};
+  size_t bytes = 0;
+  int rc = g_entry.mx_logits_ws(&p, &bytes);
+  if (rc != FLCE_OK) return status(rc);
+  Tensor ws;
+  if (!workspace(a[9], bytes, *h.t, &ws)) Py_RETURN_NONE;
+  rc = g_entry.mx_logits(&p, h.ptr(), w.codes.ptr(), w.scales.ptr(), bias.ptr(),
+                         out.numel() ? out.data_ptr() : nullptr, ws.data_ptr(), bytes, stream_of(*h.t));
+  if (rc != FLCE_OK) return status(rc);
+  if (given) wrote(out);
+  PyObject* r = pack({out});
+  if (r && given) {  // the caller's own object
+    Py_INCREF(a[8]);
+    PyTuple_SetItem(r, 0, a[8]);
+  }
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
+// (logits, uniform, temperature, top_k, top_p, min_p) -> (token, logprob, kept)
+PyObject* sample_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 6) return PyErr_Format(PyExc_TypeError, "sample_tokens takes 6 arguments");
+  const Arg z = arg(a[0]);
+  if (!z || !z.ok || z->dim() != 2) Py_RETURN_NONE;
+  const Rows rows(*z.t);
+  const int code = code_of(z->scalar_type());
+  if (!rows.ok || code < 0) Py_RETURN_NONE;
+  Arg t[5];
+  for (int i = 0; i < 5; ++i) {
+    t[i] = arg(a[i + 1], z->get_device());
+    if (!t[i].ok || (!t[i] && i == 0) || (t[i] && !vector_of(t[i], rows.n, i == 2 ? at::kLong : at::kFloat)))
+      Py_RETURN_NONE;
+  }
+  const Tensor token = empty({rows.n}, at::kLong, *z.t), logprob = empty({rows.n}, at::kFloat, *z.t),
+               kept = empty({rows.n}, at::kLong, *z.t);
+  const bool any = rows.n > 0;
+  const flce_sample_problem p = {rows.n, rows.d, rows.stride, code, 0};
+  auto f = [](const Arg& x) { return static_cast<const float*>(x.ptr()); };
+  const int rc = g_entry.sample(&p, z.ptr(), f(t[0]), f(t[1]), static_cast<const int64_t*>(t[2].ptr()), f(t[3]), f(t[4]),
+                                any ? token.mutable_data_ptr<int64_t>() : nullptr,
+                                any ? logprob.mutable_data_ptr<float>() : nullptr,
+                                any ? kept.mutable_data_ptr<int64_t>() : nullptr, stream_of(*z.t));
+  if (rc != FLCE_OK) return status(rc);
+  return pack({token, logprob, kept});
+  END_HANDLE_TH_ERRORS
+}
+
 #define FLCE_METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {FLCE_METHOD(bind), FLCE_METHOD(add_rms_norm), FLCE_METHOD(add_rms_norm_backward),
-                          FLCE_METHOD(clip_grad_norm), FLCE_METHOD(process_logits), {nullptr, nullptr, 0, nullptr}};
+                          FLCE_METHOD(clip_grad_norm), FLCE_METHOD(process_logits), FLCE_METHOD(embedding),
+                          FLCE_METHOD(embedding_backward), FLCE_METHOD(mxfp4_quantize), FLCE_METHOD(mxfp4_dequantize),
+                          FLCE_METHOD(mxfp4_logits), FLCE_METHOD(sample_tokens), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "flce_torch", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

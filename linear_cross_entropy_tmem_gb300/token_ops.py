@@ -6,7 +6,8 @@
 * :func:`sample_tokens`: temperature, top-k, top-p and min-p on logits, and the token that a given random number chooses.
 
 As in ``head_ops.py``, PyTorch provides device memory and the current stream, every step runs in ``libflce.so``, and
-there is no CPU path.  See ``include/flce.h`` for the formulas.
+there is no CPU path.  See ``include/flce.h`` for the formulas.  Tensors that are as the library wants them are
+marshalled by ``flce_torch``; it returns None for the others, which the code here views as rows, or refuses.
 """
 from __future__ import annotations
 
@@ -18,7 +19,7 @@ import torch
 from torch.autograd.graph import increment_version
 
 from . import binding as B
-from .head_ops import _addr, _adjacent, _code, _on, _rows, _stream, _workspace
+from .head_ops import _addr, _adjacent, _call, _code, _on, _rows, _stream, _workspace
 from .once import once
 
 _IDS = (torch.int64, torch.int32)
@@ -40,6 +41,10 @@ def _flat_ids(ids):
     return ids.numel()
 
 
+def _want(dtype, what):
+    return -1 if dtype is None else _code(dtype, what)
+
+
 def _pad(padding_idx):
     return -1 if padding_idx is None else int(padding_idx)
 
@@ -49,6 +54,9 @@ def flce_embedding(weight: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.
     """``weight[ids] * scale`` (see ``flce_embedding`` in include/flce.h): [..., D] for ids of any shape.  Rows of ids
     outside [0, V), such as the -1 of :func:`process_logits` and :func:`sample_tokens`, are zeros.  ``out_dtype`` is
     the weight's dtype or fp32.  The result carries no gradient: :func:`embedding` is the call for autograd."""
+    res = _call("embedding", weight, ids, scale, _want(out_dtype, "out"))
+    if res is not None:
+        return res[0]
     dev = weight.device
     _on(dev, weight=weight, ids=ids)
     if weight.dim() != 2 or weight.shape[0] == 0 or weight.shape[1] == 0:
@@ -70,6 +78,10 @@ def flce_embedding_backward(dout: torch.Tensor, ids: torch.Tensor, vocab: int, *
     """Gradient [vocab, D] of the table, from that of the rows (see ``flce_embedding_backward``), in ``dtype`` (dout's).
     With ``dweight``, a matrix such as the gradient that a tied head's backward left, the rows' sums are added to it
     in place (rows without a token are left as they are), and it is returned."""
+    res = _call("embedding_backward", dout, ids, vocab, scale, _pad(padding_idx), _want(dtype, "dweight"), dweight,
+                workspace)
+    if res is not None:
+        return res[0]
     dev = dout.device
     _on(dev, dout=dout, ids=ids, dweight=dweight)
     d2 = _rows(dout, "dout")
@@ -159,6 +171,9 @@ def _mx_operand(q, device, name):
 
 def mxfp4_quantize(x: torch.Tensor) -> MxFp4:
     """``x`` [..., D] as rows in 4 bits (see ``flce_mxfp4_quantize``).  The result carries no gradient."""
+    res = _call("mxfp4_quantize", x)
+    if res is not None:
+        return MxFp4(*res, x.shape[-1])
     dev = x.device
     _on(dev, x=x)
     x2 = _rows(x, "x")
@@ -175,6 +190,9 @@ def mxfp4_quantize(x: torch.Tensor) -> MxFp4:
 
 def mxfp4_dequantize(q: MxFp4, dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """The values that ``q`` stands for, [rows, cols], rounded to ``dtype`` (fp32 and bf16 hold them exactly)."""
+    res = _call("mxfp4_dequantize", q.codes, q.scales, q.cols, _code(dtype, "out"))
+    if res is not None:
+        return res[0]
     dev = q.codes.device
     _mx_operand(q, dev, "q")
     n, d = q.shape
@@ -197,6 +215,10 @@ def mxfp4_logits(hidden: torch.Tensor, weight: MxFp4, bias: Optional[torch.Tenso
     states are quantised in the call, the product runs on both in 4 bits.  ``out_dtype`` is hidden's dtype, or any of
     the three; ``out`` a matrix of rows to write.  Nothing is recorded for autograd; a given ``out`` counts as changed
     in place."""
+    res = _call("mxfp4_logits", hidden, weight.codes, weight.scales, weight.cols, bias, logit_scale, softcap,
+                _want(out_dtype, "out"), out, workspace)
+    if res is not None:
+        return res[0]
     dev = hidden.device
     _on(dev, hidden=hidden, bias=bias, out=out)
     _mx_operand(weight, dev, "weight")
@@ -245,6 +267,9 @@ def sample_tokens(logits: torch.Tensor, uniform: torch.Tensor, *, temperature: O
     """A token for each row of logits [B, V], chosen by ``uniform`` [B] (fp32 in [0, 1)) among the entries that
     ``top_k`` [B] int64, then ``top_p``, then ``min_p`` [B] fp32 leave at ``temperature`` [B] fp32 (0: greedy); see
     ``flce_sample`` in include/flce.h.  Nothing is recorded for autograd."""
+    res = _call("sample_tokens", logits, uniform, temperature, top_k, top_p, min_p)
+    if res is not None:
+        return SampledTokens._make(res)
     dev = logits.device
     _on(dev, logits=logits, uniform=uniform, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
     if logits.dim() != 2 or logits.shape[1] == 0:
