@@ -9,11 +9,12 @@
 //
 // The gradient has three launches.  One cluster sorts the tokens by id (stable,
 // so equal ids stay in the tokens' order).  Then blocks of kChunk sorted tokens
-// sum their rows in registers; a run of one id that lies inside a chunk goes
-// straight to the table, the parts of a run that crosses a border go to fp32
-// slots.  Other blocks of the same launch write zeros to the rows that no token
-// names, so that every row is written once.  The third launch joins the parts, in
-// order.  Nothing depends on the order in which blocks run: same bits every time.
+// sum their rows in registers.  A run of one id that ends in its chunk or the one
+// behind it is the first one's block's, and goes straight to the table; the parts
+// of longer runs go to fp32 slots.  Other blocks of the same launch write zeros to
+// the rows that no token names, so that every row is written once.  The third
+// launch joins the parts, in order.  Nothing depends on the order in which blocks
+// run: same bits every time.
 #include <algorithm>
 #include <cmath>
 
@@ -35,44 +36,43 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int i64, int64_t i) {
   return i64 ? static_cast<const int64_t*>(ids)[i] : int64_t(static_cast<const int32_t*>(ids)[i]);
 }
 
-// kElems elements of a row as fp32: adjacent ones from `at` on (kVec), or one of
-// every blockDim.x from `at` on.
+// kElems elements of a row: adjacent ones from `at` on (kVec), or one of every kWide
+// from `at` on, of which the row has `count`.
+constexpr int kWide = 256;
 template <class T>
 struct Raw {
   Vec<T, kElems> v;
 };
 template <class T, bool kVec>
-__device__ __forceinline__ void load_elems(const T* row, int at, int cols, Raw<T>& r) {
+__device__ __forceinline__ void load_elems(const T* at, int count, Raw<T>& r) {
   if constexpr (kVec) {
-    if (at < cols) r.v = load_vec<T, kElems>(row + at);
+    if (count > 0) r.v = load_vec<T, kElems>(at);
   } else {
 #pragma unroll
-    for (int e = 0; e < kElems; ++e) {
-      const int c = at + e * int(blockDim.x);
-      if (c < cols) r.v.v[e] = row[c];
-    }
+    for (int e = 0; e < kElems; ++e)
+      if (e < count) r.v.v[e] = at[e * kWide];
   }
 }
 template <class O, bool kVec>
-__device__ __forceinline__ void store_elems(O* row, int at, int cols, const float (&x)[kElems]) {
+__device__ __forceinline__ void store_elems(O* at, int count, const float (&x)[kElems]) {
   if constexpr (kVec) {
-    if (at >= cols) return;
+    if (count <= 0) return;
     Vec<O, kElems> v;
 #pragma unroll
     for (int e = 0; e < kElems; ++e) v.v[e] = from_f32<O>(x[e]);
-    store_vec<O, kElems>(row + at, v);
+    store_vec<O, kElems>(at, v);
   } else {
 #pragma unroll
-    for (int e = 0; e < kElems; ++e) {
-      const int c = at + e * int(blockDim.x);
-      if (c < cols) row[c] = from_f32<O>(x[e]);
-    }
+    for (int e = 0; e < kElems; ++e)
+      if (e < count) at[e * kWide] = from_f32<O>(x[e]);
   }
 }
-// A block's columns [tile * blockDim.x * kElems, ...): the thread's first one.
+// A block's columns [tile * blockDim.x * kElems, ...): the thread's first one, and how many it has.
 template <bool kVec>
-__device__ __forceinline__ int first_col(int tile) {
-  return tile * int(blockDim.x) * kElems + int(threadIdx.x) * (kVec ? kElems : 1);
+__device__ __forceinline__ int first_col(int tile, int cols, int& count) {
+  const int at = tile * int(blockDim.x) * kElems + int(threadIdx.x) * (kVec ? kElems : 1);
+  count = at >= cols ? 0 : kVec ? kElems : min(kElems, (cols - at + kWide - 1) / kWide);
+  return at;
 }
 
 // ---------------------------------------------------------------------------
@@ -92,7 +92,8 @@ template <class T, class O, bool kVec, int kRows>
 __global__ void __launch_bounds__(256) embed_kernel(EmbedParams p) {
   const int tile = int(blockIdx.x % unsigned(p.tiles));
   const int64_t first = int64_t(blockIdx.x / unsigned(p.tiles)) * kRows;
-  const int at = first_col<kVec>(tile);
+  int cnt;
+  const int at = first_col<kVec>(tile, p.cols, cnt);
   Raw<T> r[kRows];
   bool there[kRows];
 #pragma unroll
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedParams p) {
     const int64_t i = first + k;
     const int64_t id = i < p.tokens ? id_at(p.ids, p.ids_i64, i) : -1;
     there[k] = id >= 0 && id < p.vocab;
-    if (there[k]) load_elems<T, kVec>(static_cast<const T*>(p.weight) + id * p.ws, at, p.cols, r[k]);
+    if (there[k]) load_elems<T, kVec>(static_cast<const T*>(p.weight) + id * p.ws + at, cnt, r[k]);
   }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedParams p) {
     float x[kElems];
 #pragma unroll
     for (int e = 0; e < kElems; ++e) x[e] = there[k] ? __fmul_rn(to_f32(r[k].v.v[e]), p.scale) : 0.f;
-    store_elems<O, kVec>(static_cast<O*>(p.out) + (first + k) * p.os, at, p.cols, x);
+    store_elems<O, kVec>(static_cast<O*>(p.out) + (first + k) * p.os + at, cnt, x);
   }
 }
 
@@ -135,10 +136,20 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
   return v;
 }
 
+// The lanes of `among` (this one is of it) with the same `width` bits in d.  (A ballot
+// for each bit: a match over the warp takes some 37 cycles of the SM.)
+__device__ __forceinline__ uint32_t same_digit(uint32_t among, uint32_t d, int width) {
+  for (int b = 0; b < width; ++b) {
+    const uint32_t ones = __ballot_sync(kFull, (d >> b) & 1u);
+    among &= (d >> b) & 1u ? ones : ~ones;
+  }
+  return among;
+}
+
 // Least significant digit first.  Every warp of the cluster owns a stretch of the
-// array: it counts its digits (32 keys at a time, equal digits found by a match
-// over the warp), the counts are summed over warps, CTAs (distributed shared
-// memory) and digits, and the warp places its keys, in order.
+// array: it counts its digits, 32 keys at a time, the counts are summed over warps,
+// CTAs (distributed shared memory) and digits, and the warp places its keys, in
+// order.
 __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(SortParams p) {
   extern __shared__ uint32_t smem[];
   const int radix = 1 << p.width;
@@ -161,37 +172,55 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(SortParams
     const bool counts = id >= 0 && id < p.vocab && id != p.padding;
     return uint64_t(counts ? id : p.vocab) << 32 | uint64_t(i);
   };
+  constexpr int kBatch = 4;  // keys of a lane under way at once
+  uint64_t key[kBatch];
+  uint32_t rank_of[kBatch];  // the key's place among the warp's of its digit
+  const bool once = per <= 32 * kBatch;  // the warp's keys and ranks stay in registers
+  auto fetch = [&](int64_t i0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) key[u] = i0 + u * 32 + lane < hi ? key_at(i0 + u * 32 + lane) : 0ull;
+  };
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = 32 + pass * p.width;
     for (int d = lane; d < radix; d += 32) mine[d] = 0u;
     __syncwarp();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const bool in = i < hi;
-      const uint32_t d = in ? uint32_t(key_at(i) >> shift) & uint32_t(radix - 1) : kFull;
-      const uint32_t same = __match_any_sync(kFull, d);
-      if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
-      __syncwarp();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kBatch) {
+      fetch(i0);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (i0 + u * 32 >= hi) break;
+        const bool in = i0 + u * 32 + lane < hi;
+        const uint32_t d = uint32_t(key[u] >> shift) & uint32_t(radix - 1);
+        const uint32_t same = same_digit(__ballot_sync(kFull, in), d, p.width);
+        rank_of[u] = mine[d] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
+        __syncwarp();
+      }
     }
     __syncthreads();
     const int d = int(threadIdx.x);
     if (d < radix) {
-      uint32_t s = 0;
-#pragma unroll 8
+      uint32_t c[kSortWarps], s = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) c[w] = count[w * radix + d];
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = count[w * radix + d];
         count[w * radix + d] = s;
-        s += c;
+        s += c[w];
       }
       total[d] = s;
     }
     cluster_sync();
     uint32_t before = 0, all = 0;
     if (d < radix) {
-      for (int c = 0; c < ctas; ++c) {
-        const uint32_t v = ld_cluster(map_to_cta(smem_u32(total + d), uint32_t(c)));
-        if (c < rank) before += v;
-        all += v;
+      uint32_t v[kSortCtas];  // (all under way at once)
+#pragma unroll
+      for (int c = 0; c < kSortCtas; ++c) v[c] = c < ctas ? ld_cluster(map_to_cta(smem_u32(total + d), uint32_t(c))) : 0u;
+#pragma unroll
+      for (int c = 0; c < kSortCtas; ++c) {
+        if (c < rank) before += v[c];
+        all += v[c];
       }
     }
     // exclusive sum of `all` over the digits
@@ -207,16 +236,23 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(SortParams
     prior = __reduce_add_sync(kFull, prior);
     if (d < radix) base[d] = prior + incl - all + before;
     __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const bool in = i < hi;
-      const uint64_t key = in ? key_at(i) : 0ull;
-      const uint32_t g = in ? uint32_t(key >> shift) & uint32_t(radix - 1) : kFull;
-      const uint32_t same = __match_any_sync(kFull, g);
-      if (in) dst[base[g] + mine[g] + __popc(same & ((1u << lane) - 1u))] = key;
-      __syncwarp();
-      if (in && lane == __ffs(same) - 1) mine[g] += __popc(same);
-      __syncwarp();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kBatch) {
+      if (!once) fetch(i0);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (i0 + u * 32 >= hi) break;
+        const bool in = i0 + u * 32 + lane < hi;
+        const uint32_t g = uint32_t(key[u] >> shift) & uint32_t(radix - 1), to = base[g] + mine[g];
+        if (once) {
+          if (in) dst[to + rank_of[u]] = key[u];
+          continue;
+        }
+        const uint32_t same = same_digit(__ballot_sync(kFull, in), g, p.width);
+        if (in) dst[to + __popc(same & ((1u << lane) - 1u))] = key[u];
+        __syncwarp();
+        if (in && lane == __ffs(same) - 1) mine[g] += __popc(same);
+        __syncwarp();
+      }
     }
     cluster_sync();  // the keys are there, and nobody reads `total` any more
     src = dst;
@@ -260,18 +296,19 @@ __device__ __forceinline__ int64_t lower_bound(const uint64_t* sorted, int64_t l
 }
 
 template <class O, bool kVec>
-__device__ __forceinline__ void write_row(const EmbedBwdParams& p, uint32_t id, int at, const float (&acc)[kElems]) {
-  O* row = static_cast<O*>(p.dweight) + int64_t(id) * p.ws;
+__device__ __forceinline__ void write_row(const EmbedBwdParams& p, uint32_t id, int at, int count,
+                                          const float (&acc)[kElems]) {
+  O* to = static_cast<O*>(p.dweight) + int64_t(id) * p.ws + at;
   float x[kElems];
 #pragma unroll
   for (int e = 0; e < kElems; ++e) x[e] = __fmul_rn(acc[e], p.scale);
   if (p.accumulate) {
     Raw<O> old;
-    load_elems<O, kVec>(row, at, p.cols, old);
+    load_elems<O, kVec>(to, count, old);
 #pragma unroll
     for (int e = 0; e < kElems; ++e) x[e] = __fadd_rn(to_f32(old.v.v[e]), x[e]);
   }
-  store_elems<O, kVec>(row, at, p.cols, x);
+  store_elems<O, kVec>(to, count, x);
 }
 
 // Zeros to the rows [r0, r1) that no token names.
@@ -308,10 +345,11 @@ __device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, int64_t r0, 
 }
 
 template <class T, class O, bool kVec>
-__global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdParams p) {
+__global__ void __launch_bounds__(256, 3) embed_sum_kernel(EmbedBwdParams p) {
   __shared__ uint32_t named[kZeroRows / 32];
-  __shared__ uint32_t keys[kChunk + 2];
-  __shared__ uint32_t tokens[kChunk];
+  __shared__ uint32_t keys[2 * kChunk + 2];
+  __shared__ uint32_t tokens[2 * kChunk];
+  __shared__ int range[4];
   griddep_wait();  // the tokens are sorted
   griddep_release();
   const int64_t sums = int64_t(p.chunks) * p.tiles;
@@ -323,48 +361,76 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdParams p) {
   const int tile = int(blockIdx.x % unsigned(p.tiles));
   const int chunk = int(blockIdx.x / unsigned(p.tiles));
   const int64_t begin = int64_t(chunk) * kChunk;
-  const int len = int(min(int64_t(kChunk), p.n - begin));
-  const int at = first_col<kVec>(tile);
-  // keys[1 + j] is the chunk's j-th; before and after it, those of its neighbours
-  if (threadIdx.x < kChunk) {
-    const int j = int(threadIdx.x);
-    const uint64_t e = j < len ? p.sorted[begin + j] : ~0ull;
-    keys[1 + j] = key_of(e);
-    tokens[j] = uint32_t(e);
-    if (j == 0) keys[0] = begin > 0 ? key_of(p.sorted[begin - 1]) : kFull;
-    if (j == 1) keys[kChunk + 1] = begin + kChunk < p.n ? key_of(p.sorted[begin + kChunk]) : kFull;
+  int count;
+  const int at = first_col<kVec>(tile, p.cols, count);
+  const T* dout = static_cast<const T*>(p.dout) + at;
+  if (threadIdx.x < 32) {
+    // keys[1 + j] is the chunk's j-th, those of the next one behind them; before and after them, their neighbours
+    const int lane = int(threadIdx.x);
+    auto entry = [&](int64_t i) { return i >= 0 && i < p.n ? p.sorted[i] : ~0ull; };
+    const uint64_t e0 = entry(begin + lane), e1 = entry(begin + kChunk + lane);
+    const uint32_t k0 = key_of(e0), k1 = key_of(e1);
+    // lane 0: before the chunk, 1: behind the two, 2: the chunk before's first, 3: before that
+    const uint32_t other = lane < 4 ? key_of(entry(lane == 0 ? begin - 1 : lane == 1 ? begin + 2 * kChunk
+                                                  : lane == 2 ? begin - kChunk : begin - kChunk - 1)) : 0u;
+    const uint32_t before = __shfl_sync(kFull, other, 0), behind = __shfl_sync(kFull, other, 1);
+    const uint32_t prior = __shfl_sync(kFull, other, 2), prior2 = __shfl_sync(kFull, other, 3);
+    keys[1 + lane] = k0;
+    keys[1 + kChunk + lane] = k1;
+    tokens[lane] = uint32_t(e0);
+    tokens[kChunk + lane] = uint32_t(e1);
+    if (lane == 0) keys[0] = before;
+    if (lane == 1) keys[2 * kChunk + 1] = behind;
+    // The run that enters: how far it goes here, and whether it began in the chunk before and ends
+    // here (its block's then).  The one that leaves: how far it goes into the next chunk, and
+    // whether it ends there (this block's then).
+    const uint32_t first = __shfl_sync(kFull, k0, 0), last = __shfl_sync(kFull, k0, 31);
+    const uint32_t m0 = ~__ballot_sync(kFull, k0 == first), m1 = ~__ballot_sync(kFull, k1 == last);
+    const int head = m0 ? __ffs(m0) - 1 : 32, ahead = m1 ? __ffs(m1) - 1 : 32;
+    const uint32_t next = __shfl_sync(kFull, k1, 0);
+    if (lane == 0) {
+      const bool enters = before == first;
+      const bool ends_here = head < 32 || next != first;
+      const bool began = prior != first || prior2 != first;
+      const bool skips = enters && ends_here && began;
+      const bool leaves = next == last && !(enters && head == 32);
+      const bool ends_next = ahead < 32 || behind != last;
+      range[0] = skips ? head : 0;
+      range[1] = kChunk + (leaves && ends_next ? ahead : 0);
+      range[2] = enters && !skips ? head - 1 : -1;       // the entering run's last token, if its part is formed here
+      range[3] = leaves && !ends_next ? kChunk - 1 : -1;  // the leaving run's
+    }
   }
   __syncthreads();
-  const uint32_t none = uint32_t(p.vocab);  // the key of tokens without a gradient
-  const bool enters = keys[0] == keys[1];
+  const uint32_t none = uint32_t(p.vocab);  // the key of tokens without a gradient; those behind the last are above it
+  const int end = range[1], enters = range[2], leaves = range[3];
   float* part = p.part + int64_t(chunk) * 2 * p.cols;
   float acc[kElems];
 #pragma unroll
   for (int e = 0; e < kElems; ++e) acc[e] = 0.f;
-  bool inside = false;  // the current run began in this chunk
-  for (int j0 = 0; j0 < len; j0 += kAhead) {
-    if (keys[1 + j0] == none) break;
+  for (int j0 = range[0]; j0 < end; j0 += kAhead) {
+    if (keys[1 + j0] >= none) break;
     Raw<T> r[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-      if (j0 + u < len && keys[1 + j0 + u] != none)
-        load_elems<T, kVec>(static_cast<const T*>(p.dout) + int64_t(tokens[j0 + u]) * p.ds, at, p.cols, r[u]);
+      if (j0 + u < end && keys[1 + j0 + u] < none)
+        load_elems<T, kVec>(dout + int64_t(tokens[j0 + u]) * p.ds, count, r[u]);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int j = j0 + u;
+      if (j >= end) break;
       const uint32_t key = keys[1 + j];
-      if (j >= len || key == none) break;
-      if (j == 0 ? !enters : key != keys[j]) inside = true;
+      if (key >= none) break;
 #pragma unroll
       for (int e = 0; e < kElems; ++e) acc[e] += to_f32(r[u].v.v[e]);
-      if (keys[2 + j] == key && j + 1 < len) continue;
-      // the run ends here, or the chunk does
-      const bool leaves = keys[2 + j] == key;
-      if (!inside || leaves) {
-        store_elems<float, kVec>(part + (inside ? p.cols : 0), at, p.cols, acc);
-        if (inside && tile == 0 && threadIdx.x == 0) p.joins[1 + atomicAdd(p.joins, 1u)] = uint32_t(chunk);
+      if (keys[2 + j] == key && j + 1 < end) continue;
+      // the run ends here, or what this block has of it
+      if (j == enters || j == leaves) {
+        const bool out = j != enters;
+        store_elems<float, kVec>(part + (out ? p.cols : 0) + at, count, acc);
+        if (out && tile == 0 && threadIdx.x == 0) p.joins[1 + atomicAdd(p.joins, 1u)] = uint32_t(chunk);
       } else {
-        write_row<O, kVec>(p, key, at, acc);
+        write_row<O, kVec>(p, key, at, count, acc);
       }
 #pragma unroll
       for (int e = 0; e < kElems; ++e) acc[e] = 0.f;
@@ -372,8 +438,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdParams p) {
   }
 }
 
-// Runs that cross a border: the part of the chunk in which the run begins and
-// those of the chunks that it enters.  kJoinWarps warps take every kJoinWarps-th
+// Runs of more than two chunks: the part of the chunk in which the run begins
+// and those of the chunks that it enters.  kJoinWarps warps take every kJoinWarps-th
 // part each, for 32 columns; their sums are added in order.
 constexpr int kJoinWarps = 8;
 template <class O>
@@ -384,17 +450,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(EmbedBwdPar
   const int tiles = (p.cols + 31) / 32;
   const int64_t work = int64_t(*p.joins) * tiles;
   for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
-    const int chunk = int(p.joins[1 + w / tiles]);
-    const int c = int(w % tiles) * 32 + lane;
-    const int64_t last = min(p.n, (int64_t(chunk) + 1) * kChunk) - 1;
-    const uint32_t id = key_of(p.sorted[last]);
-    const int64_t end = lower_bound(p.sorted, last, p.n, id + 1);  // one past the run
-    const int parts = int((end - 1) / kChunk) - chunk + 1;
+    const int chunk = int(p.joins[1 + w / tiles]), c = int(w % tiles) * 32 + lane;
+    const uint32_t id = key_of(p.sorted[(int64_t(chunk) + 1) * kChunk - 1]);
+    int parts = 1;  // the chunks that begin with the id, from the next one on
+    for (uint32_t m = kFull; m == kFull;) {
+      const int64_t i = (int64_t(chunk) + parts + lane) * kChunk;
+      m = __ballot_sync(kFull, i < p.n && key_of(p.sorted[i]) == id);
+      parts += m == kFull ? 32 : __ffs(~m) - 1;
+    }
     float s = 0.f;
     if (c < p.cols) {
-#pragma unroll 4
-      for (int i = warp; i < parts; i += kJoinWarps)
-        s += p.part[(int64_t(chunk + i) * 2 + (i == 0)) * p.cols + c];
+#pragma unroll 8
+      for (int i = warp; i < parts; i += kJoinWarps) s += p.part[(int64_t(chunk + i) * 2 + (i == 0)) * p.cols + c];
     }
     buf[warp][lane] = s;
     __syncthreads();
@@ -423,8 +490,8 @@ int validate(const flce_embedding_problem* p) {
   return FLCE_OK;
 }
 
-// Threads of a block whose threads hold kElems columns each.
-int row_threads(int64_t cols) { return int(std::min<int64_t>(256, cdiv(cdiv(cols, kElems), 32) * 32)); }
+// Threads of a block whose threads hold kElems columns each (kWide where these are apart).
+int row_threads(int64_t cols, bool vec) { return vec ? int(std::min<int64_t>(256, cdiv(cdiv(cols, kElems), 32) * 32)) : kWide; }
 
 // Whether all rows start on a boundary of kElems elements, so that vectors do.
 bool whole_vectors(int64_t cols, const void* p, int64_t stride, const void* q, int64_t stride2) {
@@ -448,7 +515,7 @@ BwdLayout bwd_layout(const flce_embedding_problem* p) {
 
 template <class T, class O, bool kVec>
 cudaError_t launch_embed(EmbedParams& q, cudaStream_t st) {
-  const int threads = row_threads(q.cols);
+  const int threads = row_threads(q.cols, kVec);
   q.tiles = int32_t(cdiv(q.cols, int64_t(threads) * kElems));
   // four rows at once where that leaves enough blocks for every SM
   if (cdiv(q.tokens, 4) * q.tiles >= 1024) {
@@ -488,7 +555,7 @@ cudaError_t launch_sort(const SortParams& s, cudaStream_t st) {
 
 template <class T, class O, bool kVec>
 cudaError_t launch_sum(EmbedBwdParams& q, cudaStream_t st) {
-  const int threads = row_threads(q.cols);
+  const int threads = row_threads(q.cols, kVec);
   q.tiles = int32_t(cdiv(q.cols, int64_t(threads) * kElems));
   const int64_t clear = q.accumulate ? 0 : cdiv(q.vocab, q.zero_rows);
   return launch_dependent(embed_sum_kernel<T, O, kVec>, unsigned(int64_t(q.chunks) * q.tiles + clear), threads, st, q);
@@ -602,8 +669,8 @@ int flce_embedding_backward(const flce_embedding_problem* problem, const void* i
                                       : launch_sum<__nv_bfloat16, __nv_bfloat16>(q, st);
     return p->out_dtype == FLCE_F32 ? launch_sum<float, __half>(q, st) : launch_sum<__half, __half>(q, st);
   }));
-  if (q.chunks < 2) return FLCE_OK;  // no border to cross
-  const unsigned grid = unsigned(std::min<int64_t>(int64_t(q.chunks) * cdiv(q.cols, 32), int64_t(dev.num_sms) * 8));
+  if (q.chunks < 3) return FLCE_OK;  // no run of more than two
+  const unsigned grid = unsigned(std::min<int64_t>(int64_t(q.chunks / 3 + 1) * cdiv(q.cols, 32), int64_t(dev.num_sms) * 8));
   return logged(FLCE_LAUNCH_OTHER, st, [&] {
     if (p->weight_dtype == FLCE_F32) return launch_dependent(embed_join_kernel<float>, grid, kJoinWarps * 32, st, q);
     if (p->weight_dtype == FLCE_BF16)
