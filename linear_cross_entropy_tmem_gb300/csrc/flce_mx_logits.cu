@@ -8,6 +8,11 @@
 // 208 TMEM columns), so that a single token costs a tile of 16 columns and not of
 // 128 rows.
 //
+// Many tokens: bound by what the tiles take from L2.  There a pair of CTAs shares a
+// tile of 256 entries x 192 tokens (cta_group::2): each loads its 128 entries and half
+// of the tokens, and the leader issues for both.  2047 x 4096 x 151936: XX us, 706 with
+// tiles of 128 x 208 of one CTA.
+//
 //   warp 8     TMA producer: per stage 256 columns (128 bytes of a row, one
 //              swizzle atom) of both operands, and their scales as they lie in
 //              memory.  As many stages as fit.
@@ -31,6 +36,7 @@ namespace {
 
 constexpr int kMxM = 128;              // vocabulary entries of a tile
 constexpr int kMxMaxN = 208;           // tokens of a tile, at most: two accumulators and four stages' scales fill TMEM
+constexpr int kMxPairN = 192;          // the same for a pair of CTAs, with five stages
 constexpr int kMxK = 256;              // columns of a stage
 constexpr int kMxRow = kMxK / 2;       // bytes
 constexpr int kMxMaxStages = 10;
@@ -48,37 +54,53 @@ struct MxLogitsParams {
   int32_t stage_bytes, b_off, as_off, bs_off;
   int32_t sf_col, sf_cols;                 // TMEM columns of the scales: the first, and a stage's
   int32_t bias_dtype;
-  float scale, cap;
+  float scale, cap, inv_cap;
 };
 
-// E2M1 operands, power-of-two scales, fp32 sums, K-major, M = 128, N = n; the
-// scales of K step `half` of two are bytes 2 half and 2 half + 1 of a TMEM word.
-__device__ __forceinline__ uint32_t instr_desc_mxf4(uint32_t n, uint32_t half) {
+// E2M1 operands, power-of-two scales, fp32 sums, K-major, m x n; the scales of K step
+// `half` of two are bytes 2 half and 2 half + 1 of a TMEM word.
+__device__ __forceinline__ uint32_t instr_desc_mxf4(uint32_t m, uint32_t n, uint32_t half) {
   return (half * 2u) << 4        // B's scale byte
          | (1u << 7)             // A: e2m1
          | (1u << 10)            // B: e2m1
          | ((n >> 3) << 17)      // N / 8
          | (1u << 23)            // scales: e8m0
-         | ((kMxM >> 4) << 24)   // M / 16
+         | ((m >> 4) << 24)      // M / 16
          | (half * 2u) << 29;    // A's scale byte
 }
+template <bool kPair>
 __device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
+  if constexpr (kPair) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  }
 }
 // 512 bytes of scales (32 rows of 16 bytes) to 4 TMEM columns, the same in each
-// quarter of the lanes: lane l, column c holds the scales of row 32 c + l.
+// quarter of the lanes: lane l, column c holds the scales of row 32 c + l.  For a
+// pair, in both CTAs, each from its own memory.
+template <bool kPair>
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem) {
   uint64_t d = 0;  // no swizzle; groups of 8 rows are 128 bytes apart
   d |= static_cast<uint64_t>((smem & 0x3FFFFu) >> 4);
   d |= static_cast<uint64_t>(128 >> 4) << 32;
   d |= static_cast<uint64_t>(1) << 46;
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+  if constexpr (kPair) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+  } else {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+  }
 }
 // Untiled copy of a multiple of 16 bytes, completion counted on an mbarrier.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -86,6 +108,17 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
+}
+
+// tanh, relative error about 3 units of fp32's last place, without a branch: below 1 Lambert's
+// continued fraction to u^2 / 9, else (e - 1) / (e + 1) with e = e^(2 u); one reciprocal.
+__device__ __forceinline__ float tanh_both(float u) {
+  const float t = fminf(fmaxf(u * (2.f * kLog2e), -60.f), 60.f), e = ex2_approx(t), s = u * u;
+  const bool low = s < 1.f;
+  const float num = low ? u * fmaf(s, s + 105.f, 945.f) : e - 1.f;
+  const float den = low ? fmaf(s, fmaf(s, 15.f, 420.f), 945.f) : e + 1.f;
+  const float y = num * rcp_approx(den);
+  return u != u ? u : y;  // (the bounds of t would hide a NaN)
 }
 
 struct MxSmem {
@@ -121,13 +154,23 @@ __device__ __forceinline__ void tile_of(const MxLogitsParams& p, int u, int& m, 
   n = u - m * p.n_tiles;
 }
 
-template <class O>
+// kPair: clusters of two CTAs.  full[s] and tempty[b] are the leader's (both CTAs'
+// copies complete on the one, both CTAs' epilogue warps arrive on the other);
+// empty[s] and tfull[b] are in each CTA, a commit to each.  The scales come by
+// tensor maps too (lines of 512 bytes), as only those copies can signal the other CTA.
+template <class O, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_logits_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                     const __grid_constant__ CUtensorMap map_as, const __grid_constant__ CUtensorMap map_bs,
                      const __grid_constant__ MxLogitsParams p, int* status) {
   extern __shared__ uint8_t smem_raw[];
   const MxSmem sm = carve(smem_raw, p.stages, p.stage_bytes);
   const int warp = threadIdx.x >> 5;
+  constexpr int kCtas = kPair ? 2 : 1;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+  const int first = int(blockIdx.x) / kCtas, stride = int(gridDim.x) / kCtas;
+  const int units = p.m_tiles * p.n_tiles;
+  const int rows_b = p.tile_n / kCtas;  // tokens of the tile that this CTA loads
   if (threadIdx.x == kTmaWarp * 32) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&sm.full[s], 1);
@@ -135,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < kAccBufs; ++b) {
       mbar_init(&sm.tfull[b], 1);
-      mbar_init(&sm.tempty[b], kEpilogueWarps);
+      mbar_init(&sm.tempty[b], kCtas * kEpilogueWarps);
     }
     mbar_init(sm.drain, 1);
     sm.ctl->abort = 0u;
@@ -144,35 +187,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&map_b);
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(sm.tmem_slot, kTmemAll);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc_pair(sm.tmem_slot, kTmemAll);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(sm.tmem_slot, kTmemAll);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair) {
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
   tc_fence_after();
   const uint32_t tmem = *sm.tmem_slot;
-  const int units = p.m_tiles * p.n_tiles;
+  bool aborted = false;
 
   if (warp == kTmaWarp) {
     // ---------------------------------------------------------------- producer
     if (elect_one()) {
-      const int mine = units > int(blockIdx.x) ? (units - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
+      const int mine = units > first ? (units - 1 - first) / stride + 1 : 0;
       const int64_t steps = int64_t(mine) * p.kbs;
       // Half of a stage: the weight's (with the count of all bytes that the stage waits for), or the tokens'.
       auto load = [&](int64_t i, int stage, bool weight) {
         int m, n;
-        tile_of(p, int(blockIdx.x) + int(i / p.kbs) * int(gridDim.x), m, n);
-        const int kb = int(i % p.kbs), groups = min(2, p.groups - 2 * kb);
+        tile_of(p, first + int(i / p.kbs) * stride, m, n);
+        const int kb = int(i % p.kbs);
         uint8_t* at = sm.stage + stage * p.stage_bytes;
         uint64_t* bar = &sm.full[stage];
-        if (weight) {
-          mbar_arrive_expect_tx(bar, uint32_t((kMxM + p.tile_n) * kMxRow + groups * (1 + p.halves) * kScaleTile));
-          tma_load_2d(at, &map_a, bar, kb * kMxRow, m * kMxM);
-          bulk_load(at + p.as_off, p.a_scales + (int64_t(m) * p.groups + 2 * kb) * kScaleTile, groups * kScaleTile, bar);
+        if constexpr (kPair) {
+          const uint32_t leader = map_to_cta(smem_u32(bar), 0u);
+          const int tile = 2 * m + int(rank);
+          if (weight) {
+            if (rank == 0)
+              mbar_arrive_expect_tx(bar, uint32_t(2 * ((kMxM + rows_b) * kMxRow + 2 * (1 + p.halves) * kScaleTile)));
+            tma_load_2d_pair(at, &map_a, leader, kb * kMxRow, tile * kMxM);
+            tma_load_2d_pair(at + p.as_off, &map_as, leader, 0, tile * p.groups + 2 * kb);
+          } else {
+            tma_load_2d_pair(at + p.b_off, &map_b, leader, kb * kMxRow, n * p.tile_n + int(rank) * rows_b);
+            tma_load_2d_pair(at + p.bs_off, &map_bs, leader, 0, (n * p.groups + 2 * kb) * p.halves);
+          }
         } else {
-          tma_load_2d(at + p.b_off, &map_b, bar, kb * kMxRow, n * p.tile_n);
-          bulk_load(at + p.bs_off, p.b_scales + (int64_t(n) * p.groups + 2 * kb) * p.halves * kScaleTile,
-                    groups * p.halves * kScaleTile, bar);
+          const int groups = min(2, p.groups - 2 * kb);
+          if (weight) {
+            mbar_arrive_expect_tx(bar, uint32_t((kMxM + rows_b) * kMxRow + groups * (1 + p.halves) * kScaleTile));
+            tma_load_2d(at, &map_a, bar, kb * kMxRow, m * kMxM);
+            bulk_load(at + p.as_off, p.a_scales + (int64_t(m) * p.groups + 2 * kb) * kScaleTile, groups * kScaleTile, bar);
+          } else {
+            tma_load_2d(at + p.b_off, &map_b, bar, kb * kMxRow, n * p.tile_n);
+            bulk_load(at + p.bs_off, p.b_scales + (int64_t(n) * p.groups + 2 * kb) * p.halves * kScaleTile,
+                      groups * p.halves * kScaleTile, bar);
+          }
         }
       };
       const int ahead = int(min(int64_t(p.stages), steps));
@@ -184,7 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t i = ahead;
       if (ahead == p.stages) {
         for (; i < steps; ++i) {
-          if (!mbar_wait(&sm.empty[stage], phase, sm.ctl, status)) break;
+          if (!mbar_wait(&sm.empty[stage], phase, sm.ctl, status)) {
+            aborted = true;
+            break;
+          }
           load(i, stage, true);
           load(i, stage, false);
           if (++stage == p.stages) {
@@ -193,19 +263,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // Every copy this thread issued has to land before the CTA may exit.
-      for (int64_t j = max(int64_t(0), i - p.stages); j < i; ++j)
-        wait_teardown(&sm.full[j % p.stages], uint32_t((j / p.stages) & 1));
+      // Every copy that completes on this CTA's barriers has to land before it may exit.
+      if (rank == 0)
+        for (int64_t j = max(int64_t(0), i - p.stages); j < i; ++j)
+          wait_teardown(&sm.full[j % p.stages], uint32_t((j / p.stages) & 1));
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- issuer
-    if (elect_one()) {
-      const uint32_t idesc[2] = {instr_desc_mxf4(uint32_t(p.tile_n), 0), instr_desc_mxf4(uint32_t(p.tile_n), 1)};
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc[2] = {instr_desc_mxf4(kCtas * kMxM, uint32_t(p.tile_n), 0),
+                                 instr_desc_mxf4(kCtas * kMxM, uint32_t(p.tile_n), 1)};
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (kPair) {
+          const uint32_t at = smem_u32(bar);
+          umma_commit_pair(at);
+          umma_commit_pair(map_to_cta(at, 1u));
+        } else {
+          umma_commit(bar);
+        }
+      };
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        if (!mbar_wait(&sm.tempty[acc], acc_phase ^ 1u, sm.ctl, status)) break;
+      for (int u = first; ok && u < units; u += stride) {
+        if (!mbar_wait(&sm.tempty[acc], acc_phase ^ 1u, sm.ctl, status)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(acc * p.tile_n);
         for (int kb = 0; kb < p.kbs; ++kb) {
@@ -219,30 +303,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int groups = min(2, p.groups - 2 * kb);
           const int steps = min(4, (p.cols - kb * kMxK + 63) / 64);
           for (int g = 0; g < groups; ++g) {
-            copy_scales(sf + g * 4, at + p.as_off + g * kScaleTile);
+            copy_scales<kPair>(sf + g * 4, at + p.as_off + g * kScaleTile);
             for (int h = 0; h < p.halves; ++h)
-              copy_scales(sf + 8 + (g * p.halves + h) * 4, at + p.bs_off + (g * p.halves + h) * kScaleTile);
+              copy_scales<kPair>(sf + 8 + (g * p.halves + h) * 4, at + p.bs_off + (g * p.halves + h) * kScaleTile);
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (k < steps)
-              umma_mxf4(d, smem_desc_sw128(at + k * 32, 16, 1024), smem_desc_sw128(at + p.b_off + k * 32, 16, 1024),
-                        idesc[k & 1], sf + (k >> 1) * 4, sf + 8 + (k >> 1) * p.halves * 4, uint32_t(kb | k));
+              umma_mxf4<kPair>(d, smem_desc_sw128(at + k * 32, 16, 1024), smem_desc_sw128(at + p.b_off + k * 32, 16, 1024),
+                               idesc[k & 1], sf + (k >> 1) * 4, sf + 8 + (k >> 1) * p.halves * 4, uint32_t(kb | k));
           }
-          umma_commit(&sm.empty[stage]);
+          commit(&sm.empty[stage]);
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        umma_commit(&sm.tfull[acc]);
+        commit(&sm.tfull[acc]);
         if (++acc == kAccBufs) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
-      umma_commit(sm.drain);
+      if (!ok) aborted = true;
+      if constexpr (kPair) {
+        umma_commit_pair(smem_u32(sm.drain));
+      } else {
+        umma_commit(sm.drain);
+      }
       wait_teardown(sm.drain, 0);
     }
     __syncwarp();
@@ -252,13 +341,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t taddr = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(grp * p.tile_n);
     uint32_t phase = 0;
     int seq = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++seq) {
+    for (int u = first; u < units; u += stride, ++seq) {
       if ((seq & 1) != grp) continue;
-      if (!mbar_wait(&sm.tfull[grp], phase, sm.ctl, status)) break;
+      if (!mbar_wait(&sm.tfull[grp], phase, sm.ctl, status)) {
+        aborted = true;
+        break;
+      }
       tc_fence_after();
       int m, n;
       tile_of(p, u, m, n);
-      const int v = m * kMxM + quarter * 32 + int(lane_id());
+      const int v = (m * kCtas + int(rank)) * kMxM + quarter * 32 + int(lane_id());
       const float bias = p.bias && v < p.vocab ? load_as(p.bias, p.bias_dtype, v) : 0.f;
       const int n0 = n * p.tile_n, count = min(p.tile_n, p.tokens - n0);
       O* out = static_cast<O*>(p.out) + int64_t(n0) * p.os + v;
@@ -270,39 +362,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 32; ++j) {
           if (c + j < count && v < p.vocab) {
             float z = (__uint_as_float(r[j]) + bias) * p.scale;
-            if (p.cap > 0.f) z = p.cap * tanhf(z / p.cap);
+            if (p.cap > 0.f) z = p.cap * tanh_both(z * p.inv_cap);
             out[int64_t(c + j) * p.os] = from_f32<O>(z);
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane_id() == 0) mbar_arrive(&sm.tempty[grp]);
+      if (lane_id() == 0) {
+        if constexpr (kPair) {
+          mbar_arrive_cluster(map_to_cta(smem_u32(&sm.tempty[grp]), 0u));
+        } else {
+          mbar_arrive(&sm.tempty[grp]);
+        }
+      }
       phase ^= 1u;
     }
   }
   griddep_release();
+  if constexpr (kPair) {
+    // After an abort, copies that the other CTA issued may still be under way to this one: time to land.
+    if (aborted || sm.ctl->abort) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 100000) {
+      }
+    }
+  }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemAll);
+    if constexpr (kPair) {
+      tmem_dealloc_pair(tmem, kTmemAll);
+    } else {
+      tmem_dealloc(tmem, kTmemAll);
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
+// More tokens than one CTA's tile holds go to pairs.  (417 tokens: XX us with pairs, XX without.)
+bool use_pair(int64_t tokens) { return tokens > kMxMaxN; }
+
 struct MxPlan {
+  bool pair;
   int tile_n, n_tiles, halves, stages, stage_bytes;
   size_t codes, scales, bytes;  // places in the workspace
 };
 MxPlan plan(const flce_mxfp4_logits_problem* p) {
   MxPlan l;
-  l.n_tiles = int(std::max<int64_t>(1, mx_cdiv(p->tokens, kMxMaxN)));
-  l.tile_n = int(std::max<int64_t>(16, mx_cdiv(mx_cdiv(p->tokens, l.n_tiles), 16) * 16));
+  l.pair = use_pair(p->tokens);
+  const int most = l.pair ? kMxPairN : kMxMaxN, ctas = l.pair ? 2 : 1, unit = 16 * ctas;
+  l.n_tiles = int(std::max<int64_t>(1, mx_cdiv(p->tokens, most)));
+  l.tile_n = int(std::max<int64_t>(unit, mx_cdiv(mx_cdiv(p->tokens, l.n_tiles), unit) * unit));
   l.halves = l.tile_n > 128 ? 2 : 1;
-  l.stage_bytes = int(mx_cdiv((kMxM + l.tile_n) * kMxRow + 2 * (1 + l.halves) * kScaleTile, 1024) * 1024);
+  l.stage_bytes = int(mx_cdiv((kMxM + l.tile_n / ctas) * kMxRow + 2 * (1 + l.halves) * kScaleTile, 1024) * 1024);
   // TMEM: two accumulators, and 8 + 8 halves columns of scales for each stage
   const int by_tmem = (int(kTmemAll) - 2 * l.tile_n) / (8 + 8 * l.halves);
   l.stages = std::min({kMxMaxStages, kMxSmem / l.stage_bytes, by_tmem});
@@ -325,25 +442,38 @@ int validate(const flce_mxfp4_logits_problem* p) {
   return FLCE_OK;
 }
 
-template <class O>
-cudaError_t launch_logits(const CUtensorMap& a, const CUtensorMap& b, const MxLogitsParams& q, int* status, int num_sms,
-                          cudaStream_t st) {
-  auto kern = mx_logits_kernel<O>;
+struct MxMaps {
+  CUtensorMap a, b, as, bs;
+};
+
+template <class O, bool kPair>
+cudaError_t launch_logits(const MxMaps& m, const MxLogitsParams& q, int* status, int num_sms, cudaStream_t st) {
+  auto kern = mx_logits_kernel<O, kPair>;
   const int smem = 1024 + q.stages * q.stage_bytes + kMxBarrierBytes;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              1024 + kMxSmem + kMxBarrierBytes);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
+  constexpr int kCtas = kPair ? 2 : 1;
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(std::min(q.m_tiles * q.n_tiles, num_sms)));
+  cfg.gridDim = dim3(unsigned(std::min(q.m_tiles * q.n_tiles, num_sms / kCtas) * kCtas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, b, q, status);
+  cfg.numAttrs = kPair ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, m.a, m.b, m.as, m.bs, q, status);
+}
+template <class O>
+cudaError_t launch_logits(bool pair, const MxMaps& m, const MxLogitsParams& q, int* status, int num_sms,
+                          cudaStream_t st) {
+  return pair ? launch_logits<O, true>(m, q, status, num_sms, st) : launch_logits<O, false>(m, q, status, num_sms, st);
 }
 
 }  // namespace
@@ -380,10 +510,19 @@ int flce_mxfp4_logits(const flce_mxfp4_logits_problem* problem, const void* hidd
   const MxPlan l = plan(p);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  CUtensorMap a, b;
+  MxMaps m;
   const uint64_t row = uint64_t(mx_row_bytes(p->cols));
-  FLCE_TRY(make_byte_map(&a, codes, row, uint64_t(p->vocab), kMxRow, kMxM));
-  FLCE_TRY(make_byte_map(&b, ws + l.codes, row, uint64_t(p->tokens), kMxRow, uint32_t(l.tile_n)));
+  const int ctas = l.pair ? 2 : 1;
+  FLCE_TRY(make_byte_map(&m.a, codes, row, uint64_t(p->vocab), kMxRow, kMxM));
+  FLCE_TRY(make_byte_map(&m.b, ws + l.codes, row, uint64_t(p->tokens), kMxRow, uint32_t(l.tile_n / ctas)));
+  if (l.pair) {
+    const uint64_t lines_a = uint64_t(mx_cdiv(p->vocab, kMxM)) * uint64_t(mx_groups(p->cols));
+    const uint64_t lines_b = uint64_t(l.n_tiles) * uint64_t(l.halves) * uint64_t(mx_groups(p->cols));
+    FLCE_TRY(make_line_map(&m.as, scales, lines_a, 2));
+    FLCE_TRY(make_line_map(&m.bs, ws + l.scales, lines_b, uint32_t(2 * l.halves)));
+  } else {
+    m.as = m.bs = m.a;  // not used
+  }
   MxQuantParams h{};
   h.x = hidden;
   h.codes = ws + l.codes;
@@ -394,7 +533,7 @@ int flce_mxfp4_logits(const flce_mxfp4_logits_problem* problem, const void* hidd
   h.cols = int32_t(p->cols);
   h.tile_rows = l.tile_n;
   FLCE_TRY(logged(FLCE_LAUNCH_OTHER, st,
-                  [&] { return launch_mx_quantize(h, p->hidden_dtype, int64_t(l.n_tiles) * l.tile_n, st); }));
+                  [&] { return launch_mx_quantize(h, p->hidden_dtype, int64_t(l.n_tiles) * l.tile_n, dev.num_sms, st); }));
   MxLogitsParams q{};
   q.a_scales = static_cast<const uint8_t*>(scales);
   q.b_scales = ws + l.scales;
@@ -408,23 +547,24 @@ int flce_mxfp4_logits(const flce_mxfp4_logits_problem* problem, const void* hidd
   q.halves = l.halves;
   q.groups = int32_t(mx_groups(p->cols));
   q.kbs = int32_t(mx_cdiv(p->cols, kMxK));
-  q.m_tiles = int32_t(mx_cdiv(p->vocab, kMxM));
+  q.m_tiles = int32_t(mx_cdiv(p->vocab, kMxM * ctas));
   q.n_tiles = l.n_tiles;
   q.stages = l.stages;
   q.stage_bytes = l.stage_bytes;
   q.b_off = kMxM * kMxRow;
-  q.as_off = q.b_off + l.tile_n * kMxRow;
+  q.as_off = q.b_off + l.tile_n / ctas * kMxRow;
   q.bs_off = q.as_off + 2 * kScaleTile;
   q.sf_col = 2 * l.tile_n;
   q.sf_cols = 8 + 8 * l.halves;
   q.bias_dtype = p->bias_dtype;
   q.scale = p->logit_scale;
   q.cap = p->softcap;
+  q.inv_cap = p->softcap > 0.f ? 1.f / p->softcap : 0.f;
   int* status = reinterpret_cast<int*>(ws);
   return logged(FLCE_LAUNCH_OTHER, st, [&] {
-    if (p->out_dtype == FLCE_F32) return launch_logits<float>(a, b, q, status, dev.num_sms, st);
-    if (p->out_dtype == FLCE_BF16) return launch_logits<__nv_bfloat16>(a, b, q, status, dev.num_sms, st);
-    return launch_logits<__half>(a, b, q, status, dev.num_sms, st);
+    if (p->out_dtype == FLCE_F32) return launch_logits<float>(l.pair, m, q, status, dev.num_sms, st);
+    if (p->out_dtype == FLCE_BF16) return launch_logits<__nv_bfloat16>(l.pair, m, q, status, dev.num_sms, st);
+    return launch_logits<__half>(l.pair, m, q, status, dev.num_sms, st);
   });
 }
 

@@ -31,102 +31,163 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
   return s == 255u ? NAN : __uint_as_float(s == 0u ? 0x00400000u : s << 23);
 }
 
-// kVec: rows start on 16-byte boundaries and a lane takes eight adjacent columns, a
-// block being four lanes'; else a lane takes one column of each block.
+// A warp's work: rows r32, r32 + 32, ... of a scale tile (128 rows), a stretch of
+// columns.  r32 is the fastest index: a block's warps share scale tiles.
+struct Item {
+  int r32, seg, half;
+  int64_t tile;
+  __device__ __forceinline__ Item(int64_t i, int segs, int halves) {
+    r32 = int(i & 31);
+    const uint32_t rest = uint32_t(i >> 5), th = rest / uint32_t(segs);
+    seg = int(rest - th * uint32_t(segs));
+    const uint32_t t = th / uint32_t(halves);
+    half = int(th - t * uint32_t(halves));
+    tile = t;
+  }
+};
+
+// The largest |x| of three (|a| is one already), a NaN if there is one.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return y;
+}
+
+// Eight values of a block's row segment as codes, at `to` with its scale's byte in
+// place in `word`; a lane has eight adjacent columns, a block is four lanes'.
+__device__ __forceinline__ void quantize_adjacent(float (&y)[8], bool write, uint32_t* to, uint32_t& word) {
+  const int lane = threadIdx.x & 31;
+  float m = max_abs(max_abs(max_abs(fabsf(y[0]), y[1], y[2]), y[3], y[4]), y[5], y[6]);
+  m = max_abs(m, y[7], __shfl_xor_sync(kFull, max_abs(m, y[7], y[7]), 1));
+  m = max_abs(m, m, __shfl_xor_sync(kFull, m, 2));
+  const uint32_t s = scale_byte(__float_as_uint(m));
+  const float inv = inverse_scale(s);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] *= inv;
+  const uint32_t codes = s == 255u ? 0u : to_e2m1x8(y);
+  if (write) *to = codes;
+  uint32_t w = s << (8 * ((lane >> 2) & 3));  // blocks of no column have m = 0 and s = 0
+  w |= __shfl_xor_sync(kFull, w, 4);
+  word = w | __shfl_xor_sync(kFull, w, 8);
+}
+// The same where a lane has one column of each of eight blocks; `to` is the segment's first byte.
+__device__ __forceinline__ void quantize_apart(float (&y)[8], uint32_t blocks, uint8_t* to, uint32_t& word) {
+  const int lane = threadIdx.x & 31;
+  uint32_t w[2] = {0u, 0u}, bad = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t top = __reduce_max_sync(kFull, __float_as_uint(y[e]) & 0x7fffffffu);
+    const uint32_t s = scale_byte(top);
+    y[e] *= inverse_scale(s);
+    bad |= s == 255u ? 15u << (4 * e) : 0u;
+    w[e >> 2] |= s << (8 * (e & 3));
+  }
+  word = lane < 16 ? w[0] : w[1];
+  const uint32_t nibbles = to_e2m1x8(y) & ~bad;  // of block e at bits 4 e
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    uint32_t v = ((nibbles >> (4 * e)) & 15u) << (4 * (lane & 7));
+    v |= __shfl_xor_sync(kFull, v, 1);
+    v |= __shfl_xor_sync(kFull, v, 2);
+    v |= __shfl_xor_sync(kFull, v, 4);
+    if ((lane & 7) == 0 && e < int(blocks)) *reinterpret_cast<uint32_t*>(to + e * 16 + (lane >> 3) * 4) = v;
+  }
+}
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src, int bytes) {  // the rest of 16 as zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+
+// kVec: rows start on 16-byte boundaries.  A warp keeps the rows of kItems - 1 further
+// items under way, copied into shared memory of its own (each lane reads what it
+// copied).  128256 x 2048 bf16, where
+// the copy rate gives 98 us: 137 us; with loads to registers, 80 KB of them under way
+// on an SM, 170.
+template <class T>
+constexpr int kItems = sizeof(T) == 2 ? 4 : 2;
+template <class T>
+constexpr int kItemBytes = 4 * 32 * 8 * int(sizeof(T));
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kThreadsQ) mx_quantize_kernel(MxQuantParams p) {
+  extern __shared__ __align__(16) uint8_t ring[];
   griddep_release();
   if (p.status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * kWarpsQ + (threadIdx.x >> 5);
-  if (item >= p.items) return;
-  // r32 fastest: the warps of a block share a scale tile
-  const int r32 = int(item & 31);
-  const int64_t rest = item >> 5;
-  const int seg = int(rest % p.segs);
-  const int64_t th = rest / p.segs;
-  const int half = int(th % p.halves);
-  const int64_t tile = th / p.halves;
-  const int col0 = seg * kSeg;
-  const int64_t blocks = mx_cdiv(p.cols, kMxBlock), row_bytes = blocks * 16;
-  float x[4][8];
-  bool there[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row_bytes = (p.cols + kMxBlock - 1) / kMxBlock * 16;
+  const int64_t step = int64_t(gridDim.x) * kWarpsQ, first = int64_t(blockIdx.x) * kWarpsQ + warp;
+  // the item's rows r0, r0 + 32, ...: how many there are
+  auto rows_of = [&](const Item& it, int64_t& r0) {
+    r0 = it.tile * p.tile_rows + it.half * 128 + it.r32;
+    return int(min((min(int64_t(p.tile_rows) * (it.tile + 1), p.rows) - r0 + 31) / 32, int64_t(4)));
+  };
+  Vec<T, 8>* mine = reinterpret_cast<Vec<T, 8>*>(ring) + warp * kItems<T> * 128 + lane;  // [item][row][lane]
+  auto copy = [&](int64_t item, int slot) {
+    if (item < p.items) {
+      const Item it(item, p.segs, p.halves);
+      int64_t r0;
+      const int rows = rows_of(it, r0), c = it.seg * kSeg + lane * 8;
+      const int bytes = max(0, min(8, p.cols - c)) * int(sizeof(T));
+      const T* row = static_cast<const T*>(p.x) + r0 * p.stride + c;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int rr = half * 128 + r32 + 32 * i;
-    const int64_t r = tile * p.tile_rows + rr;
-    there[i] = rr < p.tile_rows && r < p.rows;
-    const T* row = static_cast<const T*>(p.x) + r * p.stride;
+      for (int i = 0; i < 4; ++i, row += 32 * p.stride) {
+        const int n = i < rows ? bytes : 0;
+        uint8_t* dst = reinterpret_cast<uint8_t*>(mine + slot * 128 + i * 32);
+        const uint8_t* src = n > 0 ? reinterpret_cast<const uint8_t*>(row) : static_cast<const uint8_t*>(p.x);
+        copy_async16(dst, src, min(n, 16));
+        if (sizeof(T) == 4) copy_async16(dst + 16, n > 16 ? src + 16 : static_cast<const uint8_t*>(p.x), max(n - 16, 0));
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if constexpr (kVec) {
+#pragma unroll
+    for (int k = 0; k < kItems<T> - 1; ++k) copy(first + k * step, k);
+  }
+  int slot = 0;
+  for (int64_t item = first; item < p.items; item += step) {
+    const Item it(item, p.segs, p.halves);
+    const int col0 = it.seg * kSeg;
+    int64_t r0;
+    const int rows = rows_of(it, r0);
     if constexpr (kVec) {
-      const int c = col0 + lane * 8;
-      if (there[i] && c + 8 <= p.cols) {
-        const Vec<T, 8> v = load_vec<T, 8>(row + c);
+      copy(item + (kItems<T> - 1) * step, (slot + kItems<T> - 1) % kItems<T>);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kItems<T> - 1) : "memory");
+    }
+    Vec<T, 8> apart[kVec ? 1 : 4];
+    if constexpr (!kVec) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = to_f32(v.v[e]);
+      for (int i = 0; i < 4; ++i) {
+        const T* row = static_cast<const T*>(p.x) + (r0 + 32 * i) * p.stride;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = col0 + e * 32 + lane;
+          apart[i].v[e] = i < rows && c < p.cols ? row[c] : from_f32<T>(0.f);
+        }
+      }
+    }
+    uint32_t word[4];  // the scale bytes of the row's four blocks of the lane's group
+    uint8_t* to = p.codes + r0 * row_bytes + col0 / 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i, to += int64_t(32) * row_bytes) {
+      float y[8];
+      if constexpr (kVec) {
+        const Vec<T, 8> x = mine[slot * 128 + i * 32];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = to_f32(x.v[e]);
+        quantize_adjacent(y, i < rows && col0 + (lane & ~3) * 8 < p.cols, reinterpret_cast<uint32_t*>(to) + lane, word[i]);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = there[i] && c + e < p.cols ? to_f32(row[c + e]) : 0.f;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = col0 + e * 32 + lane;
-        x[i][e] = there[i] && c < p.cols ? to_f32(row[c]) : 0.f;
+        for (int e = 0; e < 8; ++e) y[e] = to_f32(apart[i].v[e]);
+        quantize_apart(y, i < rows ? uint32_t(p.cols - col0 + 31) / 32 : 0u, to, word[i]);
       }
     }
-  }
-  uint32_t word[4][2];  // the scale bytes of the row's two groups of four blocks
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = tile * p.tile_rows + half * 128 + r32 + 32 * i;
-    uint8_t* to = p.codes + r * row_bytes + col0 / 2;
-    if constexpr (kVec) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7fffffffu);
-      top = max(top, __shfl_xor_sync(kFull, top, 1));
-      top = max(top, __shfl_xor_sync(kFull, top, 2));
-      const uint32_t s = scale_byte(top);
-      const float inv = inverse_scale(s);
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = s == 255u ? 0.f : x[i][e] * inv;
-      const uint32_t codes = to_e2m1x8(y);
-      if (there[i] && col0 + (lane & ~3) * 8 < p.cols) reinterpret_cast<uint32_t*>(to)[lane] = codes;
-      uint32_t w = s << (8 * ((lane >> 2) & 3));  // blocks of no column have top = 0 and s = 0
-      w |= __shfl_xor_sync(kFull, w, 4);
-      w |= __shfl_xor_sync(kFull, w, 8);
-      word[i][0] = __shfl_sync(kFull, w, 0);
-      word[i][1] = __shfl_sync(kFull, w, 16);
-    } else {
-      word[i][0] = word[i][1] = 0;
-      uint32_t nibbles = 0;  // of block e at bits 4 e
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t top = __reduce_max_sync(kFull, __float_as_uint(x[i][e]) & 0x7fffffffu);
-        const uint32_t s = scale_byte(top);
-        y[e] = s == 255u ? 0.f : x[i][e] * inverse_scale(s);
-        word[i][e >> 2] |= s << (8 * (e & 3));
-      }
-      nibbles = to_e2m1x8(y);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        uint32_t v = ((nibbles >> (4 * e)) & 15u) << (4 * (lane & 7));
-        v |= __shfl_xor_sync(kFull, v, 1);
-        v |= __shfl_xor_sync(kFull, v, 2);
-        v |= __shfl_xor_sync(kFull, v, 4);
-        if ((lane & 7) == 0 && there[i] && col0 + e * 32 < p.cols)
-          *reinterpret_cast<uint32_t*>(to + e * 16 + (lane >> 3) * 4) = v;
-      }
+    // a group's tile: 16 bytes for r32, four for each of the rows
+    const int group = it.seg * 2 + (lane >> 4);
+    if ((lane & 15) == 0 && group < p.groups) {
+      uint8_t* t = p.scales + ((it.tile * p.groups + group) * p.halves + it.half) * kScaleTile + it.r32 * 16;
+      *reinterpret_cast<uint4*>(t) = make_uint4(word[0], word[1], word[2], word[3]);
     }
-  }
-  // group g's tile: 16 bytes for r32, four for each of the rows
-  if (lane < 2 && seg * 2 + lane < p.groups) {
-    uint8_t* t = p.scales + ((tile * p.groups + seg * 2 + lane) * p.halves + half) * kScaleTile + r32 * 16;
-    const uint4 v = lane == 0 ? make_uint4(word[0][0], word[1][0], word[2][0], word[3][0])
-                              : make_uint4(word[0][1], word[1][1], word[2][1], word[3][1]);
-    *reinterpret_cast<uint4*>(t) = v;
+    slot = (slot + 1) % kItems<T>;
   }
 }
 
@@ -142,35 +203,46 @@ __device__ __forceinline__ float2 from_e2m1x2(uint32_t byte) {
 struct MxDequantParams {
   const uint8_t *codes, *scales;
   void* out;
-  int64_t stride, rows;
-  int32_t cols, groups, octets;  // octets: of eight columns in a row
+  int64_t stride, rows, items;
+  int32_t cols, groups, segs;
 };
 
+// The same warps' work as above; a lane has eight adjacent columns.
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kThreadsQ) mx_dequantize_kernel(MxDequantParams p) {
-  const int64_t at = int64_t(blockIdx.x) * kThreadsQ + threadIdx.x;
-  const int64_t r = at / p.octets;
-  if (r >= p.rows) return;
-  const int oct = int(at - r * p.octets), c = oct * 8, b = oct >> 2;
-  const int64_t row_bytes = mx_cdiv(p.cols, kMxBlock) * 16;
-  const uint32_t codes = *reinterpret_cast<const uint32_t*>(p.codes + r * row_bytes + oct * 4);
-  const uint32_t s =
-      p.scales[((r >> 7) * p.groups + (b >> 2)) * kScaleTile + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (b & 3)];
-  const float scale = scale_value(s);
-  Vec<T, 8> v;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = int64_t(blockIdx.x) * kWarpsQ + (threadIdx.x >> 5);
+  if (item >= p.items) return;
+  const Item it(item, p.segs, 1);
+  const int c = it.seg * kSeg + lane * 8, group = it.seg * 2 + (lane >> 4);
+  if (c >= p.cols) return;
+  const int64_t row_bytes = mx_cdiv(p.cols, kMxBlock) * 16, r0 = it.tile * 128 + it.r32;
+  const uint4 s4 = *reinterpret_cast<const uint4*>(p.scales + (it.tile * p.groups + group) * kScaleTile + it.r32 * 16);
+  const uint32_t words[4] = {s4.x, s4.y, s4.z, s4.w};
+  uint32_t codes[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 x = from_e2m1x2((codes >> (8 * e)) & 0xffu);
-    v.v[2 * e] = from_f32<T>(x.x * scale);
-    v.v[2 * e + 1] = from_f32<T>(x.y * scale);
-  }
-  T* row = static_cast<T*>(p.out) + r * p.stride;
-  if (kVec && c + 8 <= p.cols) {
-    store_vec<T, 8>(row + c, v);
-  } else {
+  for (int i = 0; i < 4; ++i)
+    if (r0 + 32 * i < p.rows) codes[i] = *reinterpret_cast<const uint32_t*>(p.codes + (r0 + 32 * i) * row_bytes + c / 2);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < p.cols) row[c + e] = v.v[e];
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + 32 * i;
+    if (r >= p.rows) return;
+    const float scale = scale_value((words[i] >> (8 * ((lane >> 2) & 3))) & 0xffu);
+    Vec<T, 8> v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = from_e2m1x2((codes[i] >> (8 * e)) & 0xffu);
+      v.v[2 * e] = from_f32<T>(x.x * scale);
+      v.v[2 * e + 1] = from_f32<T>(x.y * scale);
+    }
+    T* row = static_cast<T*>(p.out) + r * p.stride;
+    if (kVec && c + 8 <= p.cols) {
+      store_vec<T, 8>(row + c, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < p.cols) row[c + e] = v.v[e];
+    }
   }
 }
 
@@ -179,18 +251,22 @@ bool whole_rows(const void* p, int64_t stride, int64_t rows, size_t es) {
 }
 
 template <class T>
-cudaError_t launch_quantize(const MxQuantParams& p, cudaStream_t st) {
-  const unsigned grid = unsigned(mx_cdiv(p.items, kWarpsQ));
+cudaError_t launch_quantize(const MxQuantParams& p, int num_sms, cudaStream_t st) {
+  const int64_t want = mx_cdiv(p.items, kWarpsQ);
   if (whole_rows(p.x, p.stride, p.rows, sizeof(T))) {
-    mx_quantize_kernel<T, true><<<grid, kThreadsQ, 0, st>>>(p);
+    auto kern = mx_quantize_kernel<T, true>;
+    constexpr int smem = kWarpsQ * kItems<T> * kItemBytes<T>;  // three blocks on an SM
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<unsigned(std::min<int64_t>(want, int64_t(num_sms) * 3)), kThreadsQ, smem, st>>>(p);
   } else {
-    mx_quantize_kernel<T, false><<<grid, kThreadsQ, 0, st>>>(p);
+    mx_quantize_kernel<T, false><<<unsigned(std::min<int64_t>(want, int64_t(num_sms) * 32)), kThreadsQ, 0, st>>>(p);
   }
   return cudaGetLastError();
 }
 template <class T>
 cudaError_t launch_dequantize(const MxDequantParams& p, cudaStream_t st) {
-  const unsigned grid = unsigned(mx_cdiv(p.rows * p.octets, kThreadsQ));
+  const unsigned grid = unsigned(mx_cdiv(p.items, kWarpsQ));
   if (whole_rows(p.out, p.stride, p.rows, sizeof(T))) {
     mx_dequantize_kernel<T, true><<<grid, kThreadsQ, 0, st>>>(p);
   } else {
@@ -203,24 +279,21 @@ int validate(const flce_mxfp4_problem* p) {
   if (!p) return FLCE_ERR_INVALID_ARG;
   if (p->rows < 0 || p->rows > INT32_MAX - 256 || p->cols < 1 || p->cols > (1 << 24) || p->stride < 0)
     return FLCE_ERR_INVALID_ARG;
-  // one warp for four rows of 256 columns
-  if (mx_cdiv(p->rows, 128) * 32 * mx_cdiv(p->cols, kSeg) > int64_t(INT32_MAX) * kWarpsQ ||
-      p->rows * mx_cdiv(p->cols, 8) > int64_t(INT32_MAX) * kThreadsQ)
-    return FLCE_ERR_INVALID_ARG;
+  if (mx_cdiv(p->rows, 128) * mx_cdiv(p->cols, kSeg) > (1 << 28)) return FLCE_ERR_INVALID_ARG;  // a grid's blocks
   if (!known_dtype(p->dtype)) return FLCE_ERR_UNSUPPORTED_DTYPE;
   return FLCE_OK;
 }
 
 }  // namespace
 
-cudaError_t launch_mx_quantize(MxQuantParams p, int dtype, int64_t rows_padded, cudaStream_t st) {
+cudaError_t launch_mx_quantize(MxQuantParams p, int dtype, int64_t rows_padded, int num_sms, cudaStream_t st) {
   p.groups = int32_t(mx_groups(p.cols));
   p.segs = int32_t(mx_cdiv(p.cols, kSeg));
   p.halves = int32_t(mx_cdiv(p.tile_rows, 128));
   p.items = mx_cdiv(rows_padded, p.tile_rows) * p.halves * p.segs * 32;
-  if (dtype == FLCE_F32) return launch_quantize<float>(p, st);
-  if (dtype == FLCE_BF16) return launch_quantize<__nv_bfloat16>(p, st);
-  return launch_quantize<__half>(p, st);
+  if (dtype == FLCE_F32) return launch_quantize<float>(p, num_sms, st);
+  if (dtype == FLCE_BF16) return launch_quantize<__nv_bfloat16>(p, num_sms, st);
+  return launch_quantize<__half>(p, num_sms, st);
 }
 
 }  // namespace flce
@@ -260,7 +333,7 @@ int flce_mxfp4_quantize(const flce_mxfp4_problem* problem, const void* x, void* 
   q.cols = int32_t(p->cols);
   q.tile_rows = 128;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return logged(FLCE_LAUNCH_OTHER, st, [&] { return launch_mx_quantize(q, p->dtype, p->rows, st); });
+  return logged(FLCE_LAUNCH_OTHER, st, [&] { return launch_mx_quantize(q, p->dtype, p->rows, dev.num_sms, st); });
 }
 
 int flce_mxfp4_dequantize(const flce_mxfp4_problem* problem, const void* codes, const void* scales, void* out,
@@ -282,7 +355,8 @@ int flce_mxfp4_dequantize(const flce_mxfp4_problem* problem, const void* codes, 
   q.rows = p->rows;
   q.cols = int32_t(p->cols);
   q.groups = int32_t(mx_groups(p->cols));
-  q.octets = int32_t(mx_cdiv(p->cols, 8));
+  q.segs = int32_t(mx_cdiv(p->cols, kSeg));
+  q.items = mx_cdiv(p->rows, 128) * q.segs * 32;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return logged(FLCE_LAUNCH_OTHER, st, [&] {
     if (p->dtype == FLCE_F32) return launch_dequantize<float>(q, st);

@@ -42,6 +42,6 @@ struct MxQuantParams {
   int32_t cols, tile_rows, halves, groups, segs;
 };
 
-cudaError_t launch_mx_quantize(MxQuantParams p, int dtype, int64_t rows_padded, cudaStream_t st);
+cudaError_t launch_mx_quantize(MxQuantParams p, int dtype, int64_t rows_padded, int num_sms, cudaStream_t st);
 
 }  // namespace flce
