@@ -68,38 +68,63 @@ __device__ __forceinline__ uint32_t instr_desc_mxf4(uint32_t m, uint32_t n, uint
          | ((m >> 4) << 24)      // M / 16
          | (half * 2u) << 29;    // A's scale byte
 }
+// These are issued by the lane with `lead`, from code that the whole warp runs: where
+// control flow is uniform the descriptors stay in uniform registers.  (Issued from one
+// thread's own branch, a stage's four copies and four MMAs took 600 cycles, more than
+// the stage's bytes: 63 us in place of XX for one token.)
 template <bool kPair>
-__device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+__device__ __forceinline__ void umma_mxf4(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t accumulate) {
   if constexpr (kPair) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
         : "memory");
   } else {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
+        : "memory");
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void commit_to(uint32_t lead, uint32_t bar) {
+  if constexpr (kPair) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"(lead)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"(lead)
         : "memory");
   }
 }
 // 512 bytes of scales (32 rows of 16 bytes) to 4 TMEM columns, the same in each
 // quarter of the lanes: lane l, column c holds the scales of row 32 c + l.  For a
 // pair, in both CTAs, each from its own memory.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem) {  // no swizzle; groups of 8 rows are 128 bytes apart
+  return static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128 >> 4) << 32 | uint64_t(1) << 46;
+}
 template <bool kPair>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem) {
-  uint64_t d = 0;  // no swizzle; groups of 8 rows are 128 bytes apart
-  d |= static_cast<uint64_t>((smem & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(128 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
+__device__ __forceinline__ void copy_scales(uint32_t lead, uint32_t taddr, uint64_t desc) {
   if constexpr (kPair) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr), "l"(desc), "r"(lead)
+        : "memory");
   } else {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr), "l"(desc), "r"(lead)
+        : "memory");
   }
 }
 // Untiled copy of a multiple of 16 bytes, completion counted on an mbarrier.
@@ -141,6 +166,32 @@ __device__ __forceinline__ MxSmem carve(uint8_t* raw, int stages, int stage_byte
 }
 constexpr int kMxBarrierBytes = 1024;
 
+// As mbar_wait, but the clock and the abort flag are looked at once in 64 tries: these waits end within a
+// microsecond, and their wake-up is on the way of every stage.
+__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, CtaControl* ctl, int* status) {
+  const uint32_t addr = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(addr, parity)) return true;
+    if (i & 63u) continue;
+    if (ctl->abort) return false;
+    const uint64_t t = global_timer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitTimeoutNs) {
+      ctl->abort = 1u;
+      if (status) atomicCAS(status, 0, kStatusTimeout);
+      return false;
+    }
+  }
+}
+
+// For a whole warp, which gives up as one (a vote is uniform).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, CtaControl* ctl, int* status) {
+  const uint32_t addr = smem_u32(bar);
+  if (__all_sync(0xffffffffu, mbar_try_wait(addr, parity))) return true;
+  return __all_sync(0xffffffffu, stage_wait(bar, parity, ctl, status));
+}
+
 // Until a copy or an MMA that this thread started has ended (bounded all the same).
 __device__ __forceinline__ void wait_teardown(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();
@@ -154,6 +205,27 @@ __device__ __forceinline__ void tile_of(const MxLogitsParams& p, int u, int& m, 
   n = u - m * p.n_tiles;
 }
 
+// A CTA's (pair's) steps, a stage each: `kbs` per tile, tiles `stride` apart.  (Counted up: the divisions
+// per stage that tile_of and kbs would take kept the producer, one thread, from its copies: 63 us
+// in place of XX for one token.)
+struct Step {
+  int m, n, kb = 0, dm, dn;
+  __device__ __forceinline__ Step(const MxLogitsParams& p, int first, int stride) {
+    tile_of(p, first, m, n);
+    tile_of(p, stride, dm, dn);
+  }
+  __device__ __forceinline__ void next(const MxLogitsParams& p) {
+    if (++kb < p.kbs) return;
+    kb = 0;
+    m += dm;
+    n += dn;
+    if (n >= p.n_tiles) {
+      n -= p.n_tiles;
+      ++m;
+    }
+  }
+};
+
 // kPair: clusters of two CTAs.  full[s] and tempty[b] are the leader's (both CTAs'
 // copies complete on the one, both CTAs' epilogue warps arrive on the other);
 // empty[s] and tfull[b] are in each CTA, a commit to each.  The scales come by
@@ -165,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ MxLogitsParams p, int* status) {
   extern __shared__ uint8_t smem_raw[];
   const MxSmem sm = carve(smem_raw, p.stages, p.stage_bytes);
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // (uniform)
   constexpr int kCtas = kPair ? 2 : 1;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u;
   const int first = int(blockIdx.x) / kCtas, stride = int(gridDim.x) / kCtas;
@@ -202,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   tc_fence_after();
-  const uint32_t tmem = *sm.tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *sm.tmem_slot, 0);
   bool aborted = false;
 
   if (warp == kTmaWarp) {
@@ -211,10 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int mine = units > first ? (units - 1 - first) / stride + 1 : 0;
       const int64_t steps = int64_t(mine) * p.kbs;
       // Half of a stage: the weight's (with the count of all bytes that the stage waits for), or the tokens'.
-      auto load = [&](int64_t i, int stage, bool weight) {
-        int m, n;
-        tile_of(p, first + int(i / p.kbs) * stride, m, n);
-        const int kb = int(i % p.kbs);
+      auto load = [&](const Step& s, int stage, bool weight) {
+        const int m = s.m, n = s.n, kb = s.kb;
         uint8_t* at = sm.stage + stage * p.stage_bytes;
         uint64_t* bar = &sm.full[stage];
         if constexpr (kPair) {
@@ -243,20 +313,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       const int ahead = int(min(int64_t(p.stages), steps));
-      for (int i = 0; i < ahead; ++i) load(i, i, true);
+      Step w(p, first, stride), t = w;
+      for (int i = 0; i < ahead; ++i, w.next(p)) load(w, i, true);
       griddep_wait();  // the hidden states are quantised, the status word is cleared
-      for (int i = 0; i < ahead; ++i) load(i, i, false);
+      for (int i = 0; i < ahead; ++i, t.next(p)) load(t, i, false);
       int stage = 0;
       uint32_t phase = 0;
       int64_t i = ahead;
       if (ahead == p.stages) {
         for (; i < steps; ++i) {
-          if (!mbar_wait(&sm.empty[stage], phase, sm.ctl, status)) {
+          if (!stage_wait(&sm.empty[stage], phase, sm.ctl, status)) {
             aborted = true;
             break;
           }
-          load(i, stage, true);
-          load(i, stage, false);
+          load(w, stage, true);
+          load(w, stage, false);
+          w.next(p);
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
@@ -270,49 +342,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- issuer
-    if (rank == 0 && elect_one()) {
-      const uint32_t idesc[2] = {instr_desc_mxf4(kCtas * kMxM, uint32_t(p.tile_n), 0),
-                                 instr_desc_mxf4(kCtas * kMxM, uint32_t(p.tile_n), 1)};
+    if (rank == 0) {
+      const uint32_t lead = elect_one() ? 1u : 0u;
+      const uint32_t idesc0 = instr_desc_mxf4(kCtas * kMxM, uint32_t(p.tile_n), 0);
+      const uint32_t idesc1 = instr_desc_mxf4(kCtas * kMxM, uint32_t(p.tile_n), 1);
       auto commit = [&](uint64_t* bar) {
-        if constexpr (kPair) {
-          const uint32_t at = smem_u32(bar);
-          umma_commit_pair(at);
-          umma_commit_pair(map_to_cta(at, 1u));
-        } else {
-          umma_commit(bar);
-        }
+        const uint32_t at = smem_u32(bar);
+        commit_to<kPair>(lead, at);
+        if constexpr (kPair) commit_to<kPair>(lead, map_to_cta(at, 1u));
       };
+      const uint32_t smem0 = smem_u32(sm.stage);
+      const uint64_t a0 = smem_desc_sw128(smem0, 16, 1024), b0 = smem_desc_sw128(smem0 + uint32_t(p.b_off), 16, 1024);
+      const uint64_t as0 = scale_desc(smem0 + uint32_t(p.as_off)), bs0 = scale_desc(smem0 + uint32_t(p.bs_off));
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int u = first; ok && u < units; u += stride) {
-        if (!mbar_wait(&sm.tempty[acc], acc_phase ^ 1u, sm.ctl, status)) {
+        if (!warp_wait(&sm.tempty[acc], acc_phase ^ 1u, sm.ctl, status)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(acc * p.tile_n);
         for (int kb = 0; kb < p.kbs; ++kb) {
-          if (!mbar_wait(&sm.full[stage], phase, sm.ctl, status)) {
+          if (!warp_wait(&sm.full[stage], phase, sm.ctl, status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t at = smem_u32(sm.stage + stage * p.stage_bytes);
+          // (descriptors hold addresses in units of 16 bytes, below 2^14 of them: sums do not carry over)
+          const uint64_t off = uint64_t(uint32_t(stage * p.stage_bytes) >> 4);
           const uint32_t sf = tmem + uint32_t(p.sf_col + stage * p.sf_cols);
-          const int groups = min(2, p.groups - 2 * kb);
-          const int steps = min(4, (p.cols - kb * kMxK + 63) / 64);
-          for (int g = 0; g < groups; ++g) {
-            copy_scales<kPair>(sf + g * 4, at + p.as_off + g * kScaleTile);
-            for (int h = 0; h < p.halves; ++h)
-              copy_scales<kPair>(sf + 8 + (g * p.halves + h) * 4, at + p.bs_off + (g * p.halves + h) * kScaleTile);
+          const int groups = p.groups - 2 * kb;
+          copy_scales<kPair>(lead, sf, as0 + off);
+          copy_scales<kPair>(lead, sf + 8, bs0 + off);
+          if (p.halves == 2) copy_scales<kPair>(lead, sf + 12, bs0 + off + kScaleTile / 16);
+          if (groups > 1) {
+            copy_scales<kPair>(lead, sf + 4, as0 + off + kScaleTile / 16);
+            copy_scales<kPair>(lead, sf + 8 + p.halves * 4, bs0 + off + p.halves * (kScaleTile / 16));
+            if (p.halves == 2) copy_scales<kPair>(lead, sf + 20, bs0 + off + 3 * (kScaleTile / 16));
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k < steps)
-              umma_mxf4<kPair>(d, smem_desc_sw128(at + k * 32, 16, 1024), smem_desc_sw128(at + p.b_off + k * 32, 16, 1024),
-                               idesc[k & 1], sf + (k >> 1) * 4, sf + 8 + (k >> 1) * p.halves * 4, uint32_t(kb | k));
-          }
+          const int left = p.cols - kb * kMxK;
+          const uint32_t sfb = sf + 8, sfb1 = sfb + p.halves * 4;
+          umma_mxf4<kPair>(lead, d, a0 + off, b0 + off, idesc0, sf, sfb, uint32_t(kb));
+          if (left > 64) umma_mxf4<kPair>(lead, d, a0 + off + 2, b0 + off + 2, idesc1, sf, sfb, 1u);
+          if (left > 128) umma_mxf4<kPair>(lead, d, a0 + off + 4, b0 + off + 4, idesc0, sf + 4, sfb1, 1u);
+          if (left > 192) umma_mxf4<kPair>(lead, d, a0 + off + 6, b0 + off + 6, idesc1, sf + 4, sfb1, 1u);
           commit(&sm.empty[stage]);
           if (++stage == p.stages) {
             stage = 0;
@@ -327,11 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) aborted = true;
-      if constexpr (kPair) {
-        umma_commit_pair(smem_u32(sm.drain));
-      } else {
-        umma_commit(sm.drain);
-      }
+      commit_to<kPair>(lead, smem_u32(sm.drain));
       wait_teardown(sm.drain, 0);
     }
     __syncwarp();
@@ -343,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int seq = 0;
     for (int u = first; u < units; u += stride, ++seq) {
       if ((seq & 1) != grp) continue;
-      if (!mbar_wait(&sm.tfull[grp], phase, sm.ctl, status)) {
+      if (!stage_wait(&sm.tfull[grp], phase, sm.ctl, status)) {
         aborted = true;
         break;
       }
