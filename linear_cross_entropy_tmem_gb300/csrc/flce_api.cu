@@ -133,17 +133,6 @@ int make_byte_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t
   return r == CUDA_SUCCESS ? FLCE_OK : FLCE_ERR_CUDA;
 }
 
-int make_line_map(CUtensorMap* m, const void* base, uint64_t lines, uint32_t box) {
-  cuuint64_t dims[2] = {128, lines};
-  cuuint64_t strides[1] = {512};
-  cuuint32_t boxes[2] = {128, box};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, boxes, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? FLCE_OK : FLCE_ERR_CUDA;
-}
-
 // The operands the tensor maps and the products address (hidden, weight, the
 // gradients, the workspace) must be memory of the current device: device
 // memory of this GPU or managed memory.  Host memory (pageable, pinned or

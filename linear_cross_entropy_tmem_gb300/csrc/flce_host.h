@@ -50,9 +50,6 @@ int check_local(const DeviceInfo& dev, const void* p, LocalRanges* known);
 int make_byte_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_inner,
                   uint32_t box_outer);
 
-// Lines of 512 bytes, `box` of them per copy, without a swizzle.
-int make_line_map(CUtensorMap* m, const void* base, uint64_t lines, uint32_t box);
-
 int log_begin(cudaStream_t st, flce_launch_record** rec);
 int log_end(int kind, cudaStream_t st, flce_launch_record* rec);
 

@@ -6,12 +6,14 @@
 // Few tokens: bound by the weight's bytes, 17/32 of V D.  The weight is the MMA's
 // A operand (128 vocabulary entries, TMEM lanes), the tokens its B operand (16 to
 // 208 TMEM columns), so that a single token costs a tile of 16 columns and not of
-// 128 rows.
+// 128 rows.  4096 x 151936: 55 us for one token (the bytes alone 49), 60 for 64, 76 for
+// 208.
 //
-// Many tokens: bound by what the tiles take from L2.  There a pair of CTAs shares a
-// tile of 256 entries x 192 tokens (cta_group::2): each loads its 128 entries and half
-// of the tokens, and the leader issues for both.  2047 x 4096 x 151936: XX us, 706 with
-// tiles of 128 x 208 of one CTA.
+// Many tokens: bound by what the tiles take from L2, 43 KB for 128 x 192 x 256, or
+// rather by the bytes under way (five stages) over the 1.7 us that a stage takes
+// around its loop: 2047 tokens take 522 us, 4.9 PFLOP/s.  (CTA pairs with tiles of
+// 256 x 192 take less from L2, but had as many bytes under way and a longer loop:
+// 553 us.)
 //
 //   warp 8     TMA producer: per stage 256 columns (128 bytes of a row, one
 //              swizzle atom) of both operands, and their scales as they lie in
@@ -36,7 +38,7 @@ namespace {
 
 constexpr int kMxM = 128;              // vocabulary entries of a tile
 constexpr int kMxMaxN = 208;           // tokens of a tile, at most: two accumulators and four stages' scales fill TMEM
-constexpr int kMxPairN = 192;          // the same for a pair of CTAs, with five stages
+constexpr int kMxManyN = 192;          // the same where there are more tiles than one: five stages fit
 constexpr int kMxK = 256;              // columns of a stage
 constexpr int kMxRow = kMxK / 2;       // bytes
 constexpr int kMxMaxStages = 10;
@@ -57,75 +59,48 @@ struct MxLogitsParams {
   float scale, cap, inv_cap;
 };
 
-// E2M1 operands, power-of-two scales, fp32 sums, K-major, m x n; the scales of K step
+// E2M1 operands, power-of-two scales, fp32 sums, K-major, M = 128, N = n; the scales of K step
 // `half` of two are bytes 2 half and 2 half + 1 of a TMEM word.
-__device__ __forceinline__ uint32_t instr_desc_mxf4(uint32_t m, uint32_t n, uint32_t half) {
+__device__ __forceinline__ uint32_t instr_desc_mxf4(uint32_t n, uint32_t half) {
   return (half * 2u) << 4        // B's scale byte
          | (1u << 7)             // A: e2m1
          | (1u << 10)            // B: e2m1
          | ((n >> 3) << 17)      // N / 8
          | (1u << 23)            // scales: e8m0
-         | ((m >> 4) << 24)      // M / 16
+         | ((kMxM >> 4) << 24)   // M / 16
          | (half * 2u) << 29;    // A's scale byte
 }
 // These are issued by the lane with `lead`, from code that the whole warp runs: where
 // control flow is uniform the descriptors stay in uniform registers.  (Issued from one
 // thread's own branch, a stage's four copies and four MMAs took 600 cycles, more than
-// the stage's bytes: 63 us in place of XX for one token.)
-template <bool kPair>
+// the stage's bytes: one token of 4096 x 151936 took 63 us in place of 55, 2047 tokens 676 in
+// place of 522.)
 __device__ __forceinline__ void umma_mxf4(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t accumulate) {
-  if constexpr (kPair) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "setp.ne.b32 q, %7, 0;\n\t"
-        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "setp.ne.b32 q, %7, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
-        : "memory");
-  }
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "setp.ne.b32 q, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
+      : "memory");
 }
-template <bool kPair>
-__device__ __forceinline__ void commit_to(uint32_t lead, uint32_t bar) {
-  if constexpr (kPair) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"(lead)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"(lead)
-        : "memory");
-  }
+__device__ __forceinline__ void commit_to(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)), "r"(lead)
+      : "memory");
 }
 // 512 bytes of scales (32 rows of 16 bytes) to 4 TMEM columns, the same in each
-// quarter of the lanes: lane l, column c holds the scales of row 32 c + l.  For a
-// pair, in both CTAs, each from its own memory.
+// quarter of the lanes: lane l, column c holds the scales of row 32 c + l.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t smem) {  // no swizzle; groups of 8 rows are 128 bytes apart
   return static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128 >> 4) << 32 | uint64_t(1) << 46;
 }
-template <bool kPair>
 __device__ __forceinline__ void copy_scales(uint32_t lead, uint32_t taddr, uint64_t desc) {
-  if constexpr (kPair) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr), "l"(desc), "r"(lead)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr), "l"(desc), "r"(lead)
-        : "memory");
-  }
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr), "l"(desc), "r"(lead)
+      : "memory");
 }
 // Untiled copy of a multiple of 16 bytes, completion counted on an mbarrier.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -205,9 +180,7 @@ __device__ __forceinline__ void tile_of(const MxLogitsParams& p, int u, int& m, 
   n = u - m * p.n_tiles;
 }
 
-// A CTA's (pair's) steps, a stage each: `kbs` per tile, tiles `stride` apart.  (Counted up: the divisions
-// per stage that tile_of and kbs would take kept the producer, one thread, from its copies: 63 us
-// in place of XX for one token.)
+// A CTA's steps, a stage each: `kbs` per tile, tiles `stride` apart; counted up, without divisions.
 struct Step {
   int m, n, kb = 0, dm, dn;
   __device__ __forceinline__ Step(const MxLogitsParams& p, int first, int stride) {
@@ -226,23 +199,14 @@ struct Step {
   }
 };
 
-// kPair: clusters of two CTAs.  full[s] and tempty[b] are the leader's (both CTAs'
-// copies complete on the one, both CTAs' epilogue warps arrive on the other);
-// empty[s] and tfull[b] are in each CTA, a commit to each.  The scales come by
-// tensor maps too (lines of 512 bytes), as only those copies can signal the other CTA.
-template <class O, bool kPair>
+template <class O>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_logits_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                     const __grid_constant__ CUtensorMap map_as, const __grid_constant__ CUtensorMap map_bs,
                      const __grid_constant__ MxLogitsParams p, int* status) {
   extern __shared__ uint8_t smem_raw[];
   const MxSmem sm = carve(smem_raw, p.stages, p.stage_bytes);
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // (uniform)
-  constexpr int kCtas = kPair ? 2 : 1;
-  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
-  const int first = int(blockIdx.x) / kCtas, stride = int(gridDim.x) / kCtas;
-  const int units = p.m_tiles * p.n_tiles;
-  const int rows_b = p.tile_n / kCtas;  // tokens of the tile that this CTA loads
+  const int units = p.m_tiles * p.n_tiles, first = int(blockIdx.x), stride = int(gridDim.x);
   if (threadIdx.x == kTmaWarp * 32) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&sm.full[s], 1);
@@ -250,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < kAccBufs; ++b) {
       mbar_init(&sm.tfull[b], 1);
-      mbar_init(&sm.tempty[b], kCtas * kEpilogueWarps);
+      mbar_init(&sm.tempty[b], kEpilogueWarps);
     }
     mbar_init(sm.drain, 1);
     sm.ctl->abort = 0u;
@@ -259,23 +223,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&map_b);
   }
   if (warp == kMmaWarp) {
-    if constexpr (kPair) {
-      tmem_alloc_pair(sm.tmem_slot, kTmemAll);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(sm.tmem_slot, kTmemAll);
-      tmem_relinquish();
-    }
+    tmem_alloc(sm.tmem_slot, kTmemAll);
+    tmem_relinquish();
   }
   tc_fence_before();
-  if constexpr (kPair) {
-    cluster_sync();
-  } else {
-    __syncthreads();
-  }
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *sm.tmem_slot, 0);
-  bool aborted = false;
 
   if (warp == kTmaWarp) {
     // ---------------------------------------------------------------- producer
@@ -287,29 +241,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int m = s.m, n = s.n, kb = s.kb;
         uint8_t* at = sm.stage + stage * p.stage_bytes;
         uint64_t* bar = &sm.full[stage];
-        if constexpr (kPair) {
-          const uint32_t leader = map_to_cta(smem_u32(bar), 0u);
-          const int tile = 2 * m + int(rank);
-          if (weight) {
-            if (rank == 0)
-              mbar_arrive_expect_tx(bar, uint32_t(2 * ((kMxM + rows_b) * kMxRow + 2 * (1 + p.halves) * kScaleTile)));
-            tma_load_2d_pair(at, &map_a, leader, kb * kMxRow, tile * kMxM);
-            tma_load_2d_pair(at + p.as_off, &map_as, leader, 0, tile * p.groups + 2 * kb);
-          } else {
-            tma_load_2d_pair(at + p.b_off, &map_b, leader, kb * kMxRow, n * p.tile_n + int(rank) * rows_b);
-            tma_load_2d_pair(at + p.bs_off, &map_bs, leader, 0, (n * p.groups + 2 * kb) * p.halves);
-          }
+        const int groups = min(2, p.groups - 2 * kb);
+        if (weight) {
+          mbar_arrive_expect_tx(bar, uint32_t((kMxM + p.tile_n) * kMxRow + groups * (1 + p.halves) * kScaleTile));
+          tma_load_2d(at, &map_a, bar, kb * kMxRow, m * kMxM);
+          bulk_load(at + p.as_off, p.a_scales + (int64_t(m) * p.groups + 2 * kb) * kScaleTile, groups * kScaleTile, bar);
         } else {
-          const int groups = min(2, p.groups - 2 * kb);
-          if (weight) {
-            mbar_arrive_expect_tx(bar, uint32_t((kMxM + rows_b) * kMxRow + groups * (1 + p.halves) * kScaleTile));
-            tma_load_2d(at, &map_a, bar, kb * kMxRow, m * kMxM);
-            bulk_load(at + p.as_off, p.a_scales + (int64_t(m) * p.groups + 2 * kb) * kScaleTile, groups * kScaleTile, bar);
-          } else {
-            tma_load_2d(at + p.b_off, &map_b, bar, kb * kMxRow, n * p.tile_n);
-            bulk_load(at + p.bs_off, p.b_scales + (int64_t(n) * p.groups + 2 * kb) * p.halves * kScaleTile,
-                      groups * p.halves * kScaleTile, bar);
-          }
+          tma_load_2d(at + p.b_off, &map_b, bar, kb * kMxRow, n * p.tile_n);
+          bulk_load(at + p.bs_off, p.b_scales + (int64_t(n) * p.groups + 2 * kb) * p.halves * kScaleTile,
+                    groups * p.halves * kScaleTile, bar);
         }
       };
       const int ahead = int(min(int64_t(p.stages), steps));
@@ -322,10 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t i = ahead;
       if (ahead == p.stages) {
         for (; i < steps; ++i) {
-          if (!stage_wait(&sm.empty[stage], phase, sm.ctl, status)) {
-            aborted = true;
-            break;
-          }
+          if (!stage_wait(&sm.empty[stage], phase, sm.ctl, status)) break;
           load(w, stage, true);
           load(w, stage, false);
           w.next(p);
@@ -335,22 +272,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // Every copy that completes on this CTA's barriers has to land before it may exit.
-      if (rank == 0)
-        for (int64_t j = max(int64_t(0), i - p.stages); j < i; ++j)
-          wait_teardown(&sm.full[j % p.stages], uint32_t((j / p.stages) & 1));
+      // Every copy this thread issued has to land before the CTA may exit.
+      for (int64_t j = max(int64_t(0), i - p.stages); j < i; ++j)
+        wait_teardown(&sm.full[j % p.stages], uint32_t((j / p.stages) & 1));
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- issuer
-    if (rank == 0) {
+    {
       const uint32_t lead = elect_one() ? 1u : 0u;
-      const uint32_t idesc0 = instr_desc_mxf4(kCtas * kMxM, uint32_t(p.tile_n), 0);
-      const uint32_t idesc1 = instr_desc_mxf4(kCtas * kMxM, uint32_t(p.tile_n), 1);
-      auto commit = [&](uint64_t* bar) {
-        const uint32_t at = smem_u32(bar);
-        commit_to<kPair>(lead, at);
-        if constexpr (kPair) commit_to<kPair>(lead, map_to_cta(at, 1u));
-      };
+      const uint32_t idesc0 = instr_desc_mxf4(uint32_t(p.tile_n), 0), idesc1 = instr_desc_mxf4(uint32_t(p.tile_n), 1);
       const uint32_t smem0 = smem_u32(sm.stage);
       const uint64_t a0 = smem_desc_sw128(smem0, 16, 1024), b0 = smem_desc_sw128(smem0 + uint32_t(p.b_off), 16, 1024);
       const uint64_t as0 = scale_desc(smem0 + uint32_t(p.as_off)), bs0 = scale_desc(smem0 + uint32_t(p.bs_off));
@@ -374,35 +304,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t off = uint64_t(uint32_t(stage * p.stage_bytes) >> 4);
           const uint32_t sf = tmem + uint32_t(p.sf_col + stage * p.sf_cols);
           const int groups = p.groups - 2 * kb;
-          copy_scales<kPair>(lead, sf, as0 + off);
-          copy_scales<kPair>(lead, sf + 8, bs0 + off);
-          if (p.halves == 2) copy_scales<kPair>(lead, sf + 12, bs0 + off + kScaleTile / 16);
+          copy_scales(lead, sf, as0 + off);
+          copy_scales(lead, sf + 8, bs0 + off);
+          if (p.halves == 2) copy_scales(lead, sf + 12, bs0 + off + kScaleTile / 16);
           if (groups > 1) {
-            copy_scales<kPair>(lead, sf + 4, as0 + off + kScaleTile / 16);
-            copy_scales<kPair>(lead, sf + 8 + p.halves * 4, bs0 + off + p.halves * (kScaleTile / 16));
-            if (p.halves == 2) copy_scales<kPair>(lead, sf + 20, bs0 + off + 3 * (kScaleTile / 16));
+            copy_scales(lead, sf + 4, as0 + off + kScaleTile / 16);
+            copy_scales(lead, sf + 8 + p.halves * 4, bs0 + off + p.halves * (kScaleTile / 16));
+            if (p.halves == 2) copy_scales(lead, sf + 20, bs0 + off + 3 * (kScaleTile / 16));
           }
           const int left = p.cols - kb * kMxK;
           const uint32_t sfb = sf + 8, sfb1 = sfb + p.halves * 4;
-          umma_mxf4<kPair>(lead, d, a0 + off, b0 + off, idesc0, sf, sfb, uint32_t(kb));
-          if (left > 64) umma_mxf4<kPair>(lead, d, a0 + off + 2, b0 + off + 2, idesc1, sf, sfb, 1u);
-          if (left > 128) umma_mxf4<kPair>(lead, d, a0 + off + 4, b0 + off + 4, idesc0, sf + 4, sfb1, 1u);
-          if (left > 192) umma_mxf4<kPair>(lead, d, a0 + off + 6, b0 + off + 6, idesc1, sf + 4, sfb1, 1u);
-          commit(&sm.empty[stage]);
+          umma_mxf4(lead, d, a0 + off, b0 + off, idesc0, sf, sfb, uint32_t(kb));
+          if (left > 64) umma_mxf4(lead, d, a0 + off + 2, b0 + off + 2, idesc1, sf, sfb, 1u);
+          if (left > 128) umma_mxf4(lead, d, a0 + off + 4, b0 + off + 4, idesc0, sf + 4, sfb1, 1u);
+          if (left > 192) umma_mxf4(lead, d, a0 + off + 6, b0 + off + 6, idesc1, sf + 4, sfb1, 1u);
+          commit_to(lead, &sm.empty[stage]);
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        commit(&sm.tfull[acc]);
+        commit_to(lead, &sm.tfull[acc]);
         if (++acc == kAccBufs) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
-      if (!ok) aborted = true;
-      commit_to<kPair>(lead, smem_u32(sm.drain));
+      commit_to(lead, sm.drain);
       wait_teardown(sm.drain, 0);
     }
     __syncwarp();
@@ -414,14 +343,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int seq = 0;
     for (int u = first; u < units; u += stride, ++seq) {
       if ((seq & 1) != grp) continue;
-      if (!stage_wait(&sm.tfull[grp], phase, sm.ctl, status)) {
-        aborted = true;
-        break;
-      }
+      if (!stage_wait(&sm.tfull[grp], phase, sm.ctl, status)) break;
       tc_fence_after();
       int m, n;
       tile_of(p, u, m, n);
-      const int v = (m * kCtas + int(rank)) * kMxM + quarter * 32 + int(lane_id());
+      const int v = m * kMxM + quarter * 32 + int(lane_id());
       const float bias = p.bias && v < p.vocab ? load_as(p.bias, p.bias_dtype, v) : 0.f;
       const int n0 = n * p.tile_n, count = min(p.tile_n, p.tokens - n0);
       O* out = static_cast<O*>(p.out) + int64_t(n0) * p.os + v;
@@ -440,57 +366,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane_id() == 0) {
-        if constexpr (kPair) {
-          mbar_arrive_cluster(map_to_cta(smem_u32(&sm.tempty[grp]), 0u));
-        } else {
-          mbar_arrive(&sm.tempty[grp]);
-        }
-      }
+      if (lane_id() == 0) mbar_arrive(&sm.tempty[grp]);
       phase ^= 1u;
     }
   }
   griddep_release();
-  if constexpr (kPair) {
-    // After an abort, copies that the other CTA issued may still be under way to this one: time to land.
-    if (aborted || sm.ctl->abort) {
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 100000) {
-      }
-    }
-  }
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_sync();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    if constexpr (kPair) {
-      tmem_dealloc_pair(tmem, kTmemAll);
-    } else {
-      tmem_dealloc(tmem, kTmemAll);
-    }
+    tmem_dealloc(tmem, kTmemAll);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-// More tokens than one CTA's tile holds go to pairs.  (417 tokens: XX us with pairs, XX without.)
-bool use_pair(int64_t tokens) { return tokens > kMxMaxN; }
-
 struct MxPlan {
-  bool pair;
   int tile_n, n_tiles, halves, stages, stage_bytes;
   size_t codes, scales, bytes;  // places in the workspace
 };
 MxPlan plan(const flce_mxfp4_logits_problem* p) {
   MxPlan l;
-  l.pair = use_pair(p->tokens);
-  const int most = l.pair ? kMxPairN : kMxMaxN, ctas = l.pair ? 2 : 1, unit = 16 * ctas;
+  const int most = p->tokens <= kMxMaxN ? kMxMaxN : kMxManyN;
   l.n_tiles = int(std::max<int64_t>(1, mx_cdiv(p->tokens, most)));
-  l.tile_n = int(std::max<int64_t>(unit, mx_cdiv(mx_cdiv(p->tokens, l.n_tiles), unit) * unit));
+  l.tile_n = int(std::max<int64_t>(16, mx_cdiv(mx_cdiv(p->tokens, l.n_tiles), 16) * 16));
   l.halves = l.tile_n > 128 ? 2 : 1;
-  l.stage_bytes = int(mx_cdiv((kMxM + l.tile_n / ctas) * kMxRow + 2 * (1 + l.halves) * kScaleTile, 1024) * 1024);
+  l.stage_bytes = int(mx_cdiv((kMxM + l.tile_n) * kMxRow + 2 * (1 + l.halves) * kScaleTile, 1024) * 1024);
   // TMEM: two accumulators, and 8 + 8 halves columns of scales for each stage
   const int by_tmem = (int(kTmemAll) - 2 * l.tile_n) / (8 + 8 * l.halves);
   l.stages = std::min({kMxMaxStages, kMxSmem / l.stage_bytes, by_tmem});
@@ -513,38 +415,25 @@ int validate(const flce_mxfp4_logits_problem* p) {
   return FLCE_OK;
 }
 
-struct MxMaps {
-  CUtensorMap a, b, as, bs;
-};
-
-template <class O, bool kPair>
-cudaError_t launch_logits(const MxMaps& m, const MxLogitsParams& q, int* status, int num_sms, cudaStream_t st) {
-  auto kern = mx_logits_kernel<O, kPair>;
+template <class O>
+cudaError_t launch_logits(const CUtensorMap& a, const CUtensorMap& b, const MxLogitsParams& q, int* status, int num_sms,
+                          cudaStream_t st) {
+  auto kern = mx_logits_kernel<O>;
   const int smem = 1024 + q.stages * q.stage_bytes + kMxBarrierBytes;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              1024 + kMxSmem + kMxBarrierBytes);
   if (e != cudaSuccess) return e;
-  constexpr int kCtas = kPair ? 2 : 1;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCtas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(std::min(q.m_tiles * q.n_tiles, num_sms / kCtas) * kCtas));
+  cfg.gridDim = dim3(unsigned(std::min(q.m_tiles * q.n_tiles, num_sms)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, m.a, m.b, m.as, m.bs, q, status);
-}
-template <class O>
-cudaError_t launch_logits(bool pair, const MxMaps& m, const MxLogitsParams& q, int* status, int num_sms,
-                          cudaStream_t st) {
-  return pair ? launch_logits<O, true>(m, q, status, num_sms, st) : launch_logits<O, false>(m, q, status, num_sms, st);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, b, q, status);
 }
 
 }  // namespace
@@ -581,19 +470,10 @@ int flce_mxfp4_logits(const flce_mxfp4_logits_problem* problem, const void* hidd
   const MxPlan l = plan(p);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  MxMaps m;
+  CUtensorMap a, b;
   const uint64_t row = uint64_t(mx_row_bytes(p->cols));
-  const int ctas = l.pair ? 2 : 1;
-  FLCE_TRY(make_byte_map(&m.a, codes, row, uint64_t(p->vocab), kMxRow, kMxM));
-  FLCE_TRY(make_byte_map(&m.b, ws + l.codes, row, uint64_t(p->tokens), kMxRow, uint32_t(l.tile_n / ctas)));
-  if (l.pair) {
-    const uint64_t lines_a = uint64_t(mx_cdiv(p->vocab, kMxM)) * uint64_t(mx_groups(p->cols));
-    const uint64_t lines_b = uint64_t(l.n_tiles) * uint64_t(l.halves) * uint64_t(mx_groups(p->cols));
-    FLCE_TRY(make_line_map(&m.as, scales, lines_a, 2));
-    FLCE_TRY(make_line_map(&m.bs, ws + l.scales, lines_b, uint32_t(2 * l.halves)));
-  } else {
-    m.as = m.bs = m.a;  // not used
-  }
+  FLCE_TRY(make_byte_map(&a, codes, row, uint64_t(p->vocab), kMxRow, kMxM));
+  FLCE_TRY(make_byte_map(&b, ws + l.codes, row, uint64_t(p->tokens), kMxRow, uint32_t(l.tile_n)));
   MxQuantParams h{};
   h.x = hidden;
   h.codes = ws + l.codes;
@@ -618,12 +498,12 @@ int flce_mxfp4_logits(const flce_mxfp4_logits_problem* problem, const void* hidd
   q.halves = l.halves;
   q.groups = int32_t(mx_groups(p->cols));
   q.kbs = int32_t(mx_cdiv(p->cols, kMxK));
-  q.m_tiles = int32_t(mx_cdiv(p->vocab, kMxM * ctas));
+  q.m_tiles = int32_t(mx_cdiv(p->vocab, kMxM));
   q.n_tiles = l.n_tiles;
   q.stages = l.stages;
   q.stage_bytes = l.stage_bytes;
   q.b_off = kMxM * kMxRow;
-  q.as_off = q.b_off + l.tile_n / ctas * kMxRow;
+  q.as_off = q.b_off + l.tile_n * kMxRow;
   q.bs_off = q.as_off + 2 * kScaleTile;
   q.sf_col = 2 * l.tile_n;
   q.sf_cols = 8 + 8 * l.halves;
@@ -633,9 +513,9 @@ int flce_mxfp4_logits(const flce_mxfp4_logits_problem* problem, const void* hidd
   q.inv_cap = p->softcap > 0.f ? 1.f / p->softcap : 0.f;
   int* status = reinterpret_cast<int*>(ws);
   return logged(FLCE_LAUNCH_OTHER, st, [&] {
-    if (p->out_dtype == FLCE_F32) return launch_logits<float>(l.pair, m, q, status, dev.num_sms, st);
-    if (p->out_dtype == FLCE_BF16) return launch_logits<__nv_bfloat16>(l.pair, m, q, status, dev.num_sms, st);
-    return launch_logits<__half>(l.pair, m, q, status, dev.num_sms, st);
+    if (p->out_dtype == FLCE_F32) return launch_logits<float>(a, b, q, status, dev.num_sms, st);
+    if (p->out_dtype == FLCE_BF16) return launch_logits<__nv_bfloat16>(a, b, q, status, dev.num_sms, st);
+    return launch_logits<__half>(a, b, q, status, dev.num_sms, st);
   });
 }
 
