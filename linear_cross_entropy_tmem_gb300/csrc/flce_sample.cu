@@ -129,11 +129,12 @@ __device__ __forceinline__ uint32_t append_cluster(uint32_t addr) {
   return v;
 }
 
-template <class N>
-__device__ __forceinline__ N warp_total(N x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-  return x;
+// Sum over a warp of numbers whose sum is below 2^63 (in limbs of 21 bits: the hardware adds 32 bits at once).
+__device__ __forceinline__ uint64_t warp_total(uint64_t x) {
+  const uint32_t a = __reduce_add_sync(kFull, uint32_t(x) & 0x1fffffu);
+  const uint32_t b = __reduce_add_sync(kFull, uint32_t(x >> 21) & 0x1fffffu);
+  const uint32_t c = __reduce_add_sync(kFull, uint32_t(x >> 42));
+  return a + (uint64_t(b) << 21) + (uint64_t(c) << 42);
 }
 template <class N>
 __device__ __forceinline__ N warp_scan(N x) {  // inclusive
@@ -144,11 +145,20 @@ __device__ __forceinline__ N warp_scan(N x) {  // inclusive
   }
   return x;
 }
-// The block's two sums of a warp's two numbers each (the same in all its lanes), and those of the warps before.
+// Over the block: the sum of one number per warp (the same in all its lanes), and that of the warps before.
 struct Sums {
-  uint64_t a, b, a_before, b_before;
+  uint64_t all, before;
 };
-__device__ __forceinline__ Sums block_sums(Shared& s, uint64_t a, uint64_t b) {
+__device__ __forceinline__ Sums block_sums(Shared& s, uint64_t a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __syncthreads();
+  if (lane == 0) s.wa[warp] = a;
+  __syncthreads();
+  const uint64_t x = s.wa[lane];
+  return {warp_total(x), warp_total(lane < warp ? x : uint64_t(0))};
+}
+// The sums of two.
+__device__ __forceinline__ void block_sums(Shared& s, uint64_t& a, uint64_t& b) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();
   if (lane == 0) {
@@ -156,22 +166,19 @@ __device__ __forceinline__ Sums block_sums(Shared& s, uint64_t a, uint64_t b) {
     s.wb[warp] = b;
   }
   __syncthreads();
-  const uint64_t x = s.wa[lane], y = s.wb[lane];
-  Sums r;
-  r.a = warp_total(x);
-  r.b = warp_total(y);
-  r.a_before = warp_total(lane < warp ? x : uint64_t(0));
-  r.b_before = warp_total(lane < warp ? y : uint64_t(0));
-  return r;
+  a = warp_total(s.wa[lane]);
+  b = warp_total(s.wb[lane]);
 }
-// Inclusive sums over the block's threads, and the whole ones.
-__device__ __forceinline__ Sums block_scan(Shared& s, uint64_t& a, uint64_t& b) {
+// Inclusive sums over the block's threads, and the whole one.
+__device__ __forceinline__ uint64_t block_scan(Shared& s, uint64_t& a) {
   a = warp_scan(a);
-  b = warp_scan(b);
-  const Sums r = block_sums(s, __shfl_sync(kFull, a, 31), __shfl_sync(kFull, b, 31));
-  a += r.a_before;
-  b += r.b_before;
-  return r;
+  const Sums r = block_sums(s, __shfl_sync(kFull, a, 31));
+  a += r.before;
+  return r.all;
+}
+__device__ __forceinline__ void block_scan(Shared& s, uint64_t& a, uint64_t& b, uint64_t& all_a, uint64_t& all_b) {
+  all_a = block_scan(s, a);
+  all_b = block_scan(s, b);
 }
 
 // A weight as factor times power of two.
@@ -440,8 +447,13 @@ __device__ __forceinline__ void descend(Shared& s, Cluster& cl, Interval& v, int
     b += m[k];
   }
   const uint64_t own_a = a, own_b = b;
-  const Sums sums = block_scan(s, a, b);
-  const Pair* all = cl.tell(sums.a, sums.b);
+  uint64_t all_a, all_b = 0;
+  if (kMass) {
+    block_scan(s, a, b, all_a, all_b);
+  } else {
+    all_a = block_scan(s, a);
+  }
+  const Pair* all = cl.tell(all_a, all_b);
   uint64_t ca = v.count + a - own_a, cb = v.mass + b - own_b;
   for (int c = 0; c < cl.rank; ++c) {
     ca += all[c].a;
@@ -585,20 +597,80 @@ __device__ __forceinline__ void write(const SampleParams& p, int64_t row, int64_
   if (p.kept) p.kept[row] = kept;
 }
 
-// The row's end where all entries that can stay are listed (n of them, at most kList):
-// one per thread, sorted by rank for the cuts, then by index for the choice.  `whole`:
-// the mass that top-p is of, if it is known to be more than the list's.  False
-// where top-p's cut lies behind the list.
+// Two numbers per lane, `lane` and `lane + 32`, in ascending order.
+__device__ __forceinline__ void warp_sort64(uint64_t (&x)[2], uint32_t n) {
+  const uint32_t lane = threadIdx.x & 31;
+  for (uint32_t k = 2; k < 2 * n; k *= 2) {
+    for (uint32_t j = k / 2; j > 0; j /= 2) {
+      if (j == 32) {  // (k = 64)
+        const uint64_t lo = min(x[0], x[1]);
+        x[1] = max(x[0], x[1]);
+        x[0] = lo;
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t y = __shfl_xor_sync(kFull, x[i], j);
+        const bool low = (((lane + 32 * i) & k) == 0) == ((lane & j) == 0);
+        x[i] = low ? min(x[i], y) : max(x[i], y);
+      }
+    }
+  }
+}
+// The row's end where all entries that can stay are listed (n of them, at most kFew, for one warp): sorted by
+// rank for the cuts, then by index for the choice.
+constexpr uint32_t kFew = 64;
+__device__ __forceinline__ void finish_few(Shared& s, const SampleParams& p, int64_t row, const Row& r,
+                                           const Weigh& weigh, uint32_t n) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint64_t x[2], w[2] = {0, 0}, upto[2] = {0, 0};
+  bool in[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) x[i] = lane + 32 * i < n ? s.list()[lane + 32 * i] : ~0ull;
+  warp_sort64(x, n);
+  auto scan = [&] {
+    upto[0] = warp_scan(w[0]);
+    upto[1] = warp_scan(w[1]) + __shfl_sync(kFull, upto[0], 31);
+    return __shfl_sync(kFull, upto[1], 31);
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t t = lane + 32 * i;
+    in[i] = t < n && (r.k == 0 || t < r.k);
+    w[i] = in[i] ? weigh(value_of(uint32_t(x[i] >> 32))) : 0ull;
+  }
+  uint64_t whole = scan();
+  const uint64_t target = r.nucleus ? r.target(whole) : ~0ull;
+  uint32_t kept = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    in[i] = in[i] && upto[i] - w[i] < target && w[i] >= r.least;
+    kept += __popc(__ballot_sync(kFull, in[i]));
+    x[i] = in[i] ? x[i] << 32 | x[i] >> 32 : ~0ull;
+  }
+  warp_sort64(x, kept);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) w[i] = lane + 32 * i < kept ? weigh(value_of(uint32_t(x[i]))) : 0ull;
+  whole = scan();
+  const uint64_t goal = r.goal(whole);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (upto[i] > goal && upto[i] - w[i] <= goal)
+      write(p, row, int64_t(x[i] >> 32), weigh.log_part(value_of(uint32_t(x[i])), whole), kept);
+}
+
+// The same for more of them (at most kList), one per thread.  `whole`: the mass that top-p is of, if it is
+// known to be more than the list's.  False where top-p's cut lies behind the list.
 __device__ __forceinline__ bool finish_list(Shared& s, const SampleParams& p, int64_t row, const Row& r,
                                             const Weigh& weigh, uint32_t n, uint64_t whole) {
   const uint32_t t = threadIdx.x;
   uint64_t x = block_sort(s.buffer(), t < n ? s.list()[t] : ~0ull, n);
   bool in = t < n && (r.k == 0 || t < r.k);
-  uint64_t w = in ? weigh(value_of(uint32_t(x >> 32))) : 0ull, upto = w, none = 0;
-  Sums sums = block_scan(s, upto, none);
+  uint64_t w = in ? weigh(value_of(uint32_t(x >> 32))) : 0ull, upto = w;
+  const uint64_t listed = block_scan(s, upto);
   if (r.nucleus) {
-    const uint64_t target = r.target(whole ? whole : sums.a);
-    if (sums.a < target) return false;
+    const uint64_t target = r.target(whole ? whole : listed);
+    if (listed < target) return false;
     in = in && upto - w < target;
   }
   in = in && w >= r.least;
@@ -608,9 +680,8 @@ __device__ __forceinline__ bool finish_list(Shared& s, const SampleParams& p, in
   const float z = value_of(uint32_t(x));
   w = in ? weigh(z) : 0ull;
   upto = w;
-  sums = block_scan(s, upto, none);
-  const uint64_t goal = r.goal(sums.a);
-  if (upto > goal && upto - w <= goal) write(p, row, int64_t(x >> 32), weigh.log_part(z, sums.a), kept);
+  const uint64_t all = block_scan(s, upto), goal = r.goal(all);
+  if (upto > goal && upto - w <= goal) write(p, row, int64_t(x >> 32), weigh.log_part(z, all), kept);
   return true;
 }
 
@@ -628,6 +699,10 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
 
   // every CTA has to run before another one writes to its memory: the wait is below
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const float temperature = p.temperature ? p.temperature[row] : 1.f;
+  const int64_t k_row = p.top_k ? p.top_k[row] : 0;
+  const float top_p = p.top_p ? p.top_p[row] : 1.f, min_p = p.min_p ? p.min_p[row] : 0.f, u = p.uniform[row];
+  for (int i = threadIdx.x; i < kBins; i += kThreadsS) s.hist[0][i] = 0u;
   if (warp == 0) {
     s.table[lane] = kTable[lane];
     const uint32_t u = uint32_t(kTable[lane] >> 31);
@@ -708,7 +783,7 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
     const int got = int(best ^ 0x80000000u);
     weigh.top = got == 0x7fffffff ? NAN : __int_as_float(got >= 0 ? got : got ^ 0x7fffffff);
   }
-  const float top = weigh.top, temperature = p.temperature ? p.temperature[row] : 1.f;
+  const float top = weigh.top;
   const bool nan = top != top;
   if (top == -INFINITY) {  // nothing is allowed
     if (out) write(p, row, -1, -INFINITY, 0);
@@ -738,13 +813,11 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
   weigh.octaves = reinterpret_cast<const uint8_t*>(&s.octaves[0][lane & 7]);
   weigh.set(temperature);
   Row r;
-  const int64_t k_row = p.top_k ? p.top_k[row] : 0;
   r.k = k_row <= 0 || k_row >= p.vocab ? 0u : uint32_t(k_row);
-  r.top_p = p.top_p ? p.top_p[row] : 1.f;
-  r.nucleus = r.top_p < 1.f;
-  const float min_p = p.min_p ? p.min_p[row] : 0.f;
+  r.top_p = top_p;
+  r.nucleus = top_p < 1.f;
   r.least = min_p > 0.f ? __float2ull_ru(fminf(min_p, 1.f) * float(1ull << p.bits)) : 0ull;
-  r.u = p.uniform[row];
+  r.u = u;
 
   // ---- where the ranking is cut: entries of smaller logits than cut_z are dropped, and those of
   // cut_z with an index above cut_i
@@ -780,7 +853,6 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
     // The first histogram, over the distance from the maximum.  Its last bin can hold most of the row: it is counted,
     // and its mass estimated, in registers.
     const float per_unit = weigh.c_hi * kBinsPerOctave;
-    clear_hist(s, 1);
     float last = 0.f;
     sl.each([&](const float (&z)[kV], int) {
 #pragma unroll
@@ -793,7 +865,7 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
         }
       }
     });
-    last = fminf(last, float(1 << 20));  // (what is not a number too)
+    last = fminf(last, 1.f);  // (what is not a number too)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) last += __shfl_xor_sync(kFull, last, o);
     if (lane == 0) atomicAdd(&s.last, __float2ull_rz(last * 0x1p32f));
@@ -825,11 +897,11 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
     constexpr int kPer = kBins / kThreadsS;
     const int bin0 = int(threadIdx.x) * kPer;
     uint32_t n[kPer];
-    uint64_t upto = 0, none = 0;
+    uint64_t upto = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) upto += n[i] = bin0 + i == kBins - 1 ? 0u : s.first[bin0 + i];
     const uint32_t mine = uint32_t(upto);
-    const uint32_t binned = uint32_t(block_scan(s, upto, none).a);
+    const uint32_t binned = uint32_t(block_scan(s, upto));
     const uint32_t before = uint32_t(upto) - mine;
     if (threadIdx.x == kThreadsS - 1) n[kPer - 1] = total - binned;
     const float tail_mass = float(s.found[3]);
@@ -869,7 +941,13 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
         });
         cluster_sync();
         if (few) {
-          if (cl.rank == 0) finish_list(s, p, row, r, weigh, v.count + v.n, 0);
+          if (cl.rank == 0) {
+            if (v.count + v.n > kFew) {
+              finish_list(s, p, row, r, weigh, v.count + v.n, 0);
+            } else if (warp == 0) {
+              finish_few(s, p, row, r, weigh, v.count + v.n);
+            }
+          }
           return;
         }
         uint64_t place = 0;
@@ -892,7 +970,7 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
       // behind the border count 1 - p and p in their difference: at most 0.0109 p (1 - p) of the
       // whole.  (That it is reached there is seen below, from exact sums.)
       const uint64_t e_mine = e_upto;
-      const float e_whole = float(block_scan(s, e_upto, none).a), goal = r.top_p * e_whole;
+      const float e_whole = float(block_scan(s, e_upto)), goal = r.top_p * e_whole;
       const float slack = e_whole * (0.0112f * fmaxf(r.top_p * (1.f - r.top_p), 0.f) + 2e-6f);
       float e_at = float(e_upto - e_mine);
       if (threadIdx.x < 2) s.at[threadIdx.x] = kBins - 1;
@@ -974,9 +1052,9 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
           }
         });
         warp_ahead = warp_total(ahead);
-        const Sums sums = block_sums(s, warp_total(whole), warp_ahead);
-        whole = sums.a;
-        ahead = sums.b;
+        whole = warp_total(whole);
+        ahead = warp_ahead;
+        block_sums(s, whole, ahead);
         cl.total(whole, ahead);
         target = r.target(whole);
         if (listing && few) {
@@ -991,7 +1069,7 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
             const uint64_t w = t < len ? weigh(value_of(uint32_t(x >> 32))) : 0ull;
             uint64_t at = w;
             if (t == 0) s.found[0] = s.found[1] = 0;
-            block_scan(s, at, none);
+            block_scan(s, at);
             s.list()[t] = x;
             if (ahead + at - w < target && ahead + at >= target) {
               s.found[0] = x;
@@ -1107,23 +1185,31 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
     sl.each(dense);
   }
   mass = warp_total(mass);
-  const Sums sums = block_sums(s, mass, warp_total(uint64_t(count)));
-  const Pair* all = cl.tell(sums.a, sums.b);
-  uint64_t whole = 0, kept = 0, ahead = 0;
-  for (int i = 0; i < cl.ctas; ++i) {
-    if (i < cl.rank) ahead += all[i].a;
-    whole += all[i].a;
-    kept += all[i].b;
+  const Sums sums = block_sums(s, mass);
+  uint64_t whole = sums.all, kept = total, ahead = 0;
+  if (listed && !r.least) {
+    kept = kept_n;
+  } else if (cut != ~0ull || r.least) {
+    kept = block_sums(s, uint64_t(__reduce_add_sync(kFull, count))).all;
   }
-  if (!r.least && cut == ~0ull) kept = total;
-  if (!r.least && listed) kept = kept_n;
+  if (cl.ctas > 1) {
+    const Pair* all = cl.tell(sums.all, kept);
+    whole = 0;
+    const bool add = (cut != ~0ull || r.least) && !(listed && !r.least);
+    if (add) kept = 0;
+    for (int i = 0; i < cl.ctas; ++i) {
+      if (i < cl.rank) ahead += all[i].a;
+      whole += all[i].a;
+      if (add) kept += all[i].b;
+    }
+  }
   const uint64_t goal = r.goal(whole);
-  if (goal < ahead || goal - ahead >= sums.a) return;  // it falls into another CTA's slice
+  if (goal < ahead || goal - ahead >= sums.all) return;  // it falls into another CTA's slice
   // the warp's part in which it falls is shared out among all warps
   __syncthreads();
-  if (lane == 0 && goal - ahead >= sums.a_before && goal - ahead - sums.a_before < mass) {
+  if (lane == 0 && goal - ahead >= sums.before && goal - ahead - sums.before < mass) {
     s.at[0] = warp;
-    s.found[0] = ahead + sums.a_before;
+    s.found[0] = ahead + sums.before;
   }
   __syncthreads();
   const int part0 = s.at[0] * sl.seg, part = cdiv(sl.seg / kStep, kWarpsS) * kStep;
@@ -1140,14 +1226,19 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
     }
     return sum;
   };
-  mass = 0;
-  sl.each(begin, end, [&](const float (&z)[kV], int j) {
-    uint64_t w[kV];
-    mass += weights(z, sl.first + j, w);
-  });
-  mass = warp_total(mass);
-  uint64_t sum = from + block_sums(s, mass, 0).a_before;
-  if (goal < sum || goal - sum >= mass) return;
+  uint64_t sum = from;
+  if (sl.seg > kStep) {
+    mass = 0;
+    sl.each(begin, end, [&](const float (&z)[kV], int j) {
+      uint64_t w[kV];
+      mass += weights(z, sl.first + j, w);
+    });
+    mass = warp_total(mass);
+    sum += block_sums(s, mass).before;
+    if (goal < sum || goal - sum >= mass) return;
+  } else if (warp > 0) {
+    return;  // it is one step, the first warp's
+  }
   bool done = false;
   sl.each(begin, end, [&](const float (&z)[kV], int j) {
     if (done) return;
@@ -1234,13 +1325,13 @@ cudaError_t launch_sample(SampleParams& q, int64_t rows, int device, cudaStream_
   if (e == cudaSuccess) e = clusters<T>(device, at_once);
   if (e != cudaSuccess) return e;
   // CTAs of a row: the least of rounds of clusters x time of a row, which is about 0.5 ns for each of a
-  // CTA's entries and 20 us (8 x 262144 fp32, top-p: 93, 58 and 44 us with 2, 4 and 8 CTAs; 256 rows of
+  // CTA's entries and 20 us, 12 without other CTAs (8 x 262144 fp32, top-p: 93, 58 and 44 us with 2, 4 and 8 CTAs; 256 rows of
   // them: 341 and 366 us with 1 and 2)
   int best = 0;
   double least = 0.0;
   for (int i = 0; i < 5; ++i) {
     if (at_once[i] <= 0) continue;
-    const double t = double(cdiv(rows, at_once[i])) * (double(cdiv(q.vocab, 1 << i)) * 0.5e-3 + 20.0);
+    const double t = double(cdiv(rows, at_once[i])) * (double(cdiv(q.vocab, 1 << i)) * 0.5e-3 + (i ? 20.0 : 12.0));
     if (least == 0.0 || t < least) {
       least = t;
       best = i;
