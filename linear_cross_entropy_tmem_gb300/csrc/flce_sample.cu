@@ -18,8 +18,8 @@
 //
 // Top-k and top-p cut the ranking at one place.  A first histogram, over the distance
 // from the maximum in steps of 2^(1/64) of the weight, names the bins in which
-// it lies.  If few entries stand up to there, one CTA lists, sorts and
-// finishes them.  Else the entries of those bins are listed and sorted, or, where
+// it lies.  If few entries stand up to there, one CTA lists and
+// finishes them.  Else the entries of those bins are listed, or, where
 // they are many (ties), found by histograms over ever smaller intervals of (value,
 // index).  The mass that top-p is of takes a pass that forms every weight, which is
 // what bounds the largest calls: 256 x 262144 fp32 with top-p takes 341 us, of which
@@ -79,9 +79,8 @@ struct Shared {
   unsigned long long last;   // mass of the first histogram's last bin, in units of 2^-32 of the largest weight
   uint32_t listed;           // length of the list
   int at[2];
-  // in place of histograms, when they are not needed: a list of entries, and room to sort it
+  // in place of a histogram, when it is not needed: a list of entries
   __device__ __forceinline__ uint64_t* list() { return reinterpret_cast<uint64_t*>(hist[0]); }
-  __device__ __forceinline__ uint64_t* buffer() { return reinterpret_cast<uint64_t*>(hist[1]); }
 };
 
 // 2^(62 - j / 32), rounded.
@@ -555,25 +554,49 @@ __device__ __forceinline__ uint32_t bin_edge(int b, float top, float per_unit) {
   return lo;
 }
 
-// The first `n` threads' numbers in ascending order (bitonic; the others' are ~0).
-__device__ __forceinline__ uint64_t block_sort(uint64_t* buf, uint64_t x, uint32_t n) {
+// Of the threads' numbers x (one each, all different; those of `in` count) within [lo, hi), in ascending order, the
+// first up to which there are, with `base`, `target` of them (kMass: of their weights w); ~0 if there is none.
+// Histograms over ever smaller intervals: two or three mostly, 1 us each.  (Sorting 1024 of them took 9 us.)
+template <bool kMass>
+__device__ __forceinline__ uint64_t block_select(Shared& s, uint64_t x, bool in, uint64_t w, uint64_t lo, uint64_t hi,
+                                                 uint64_t base, uint64_t target) {
+  uint32_t* const number = s.hist[2];
+  unsigned long long* const mass = reinterpret_cast<unsigned long long*>(s.hist[3]);
   const uint32_t t = threadIdx.x;
-  for (uint32_t k = 2; k < 2 * n; k *= 2) {
-    for (uint32_t j = k / 2; j > 0; j /= 2) {
-      uint64_t y;
-      if (j < 32) {
-        y = __shfl_xor_sync(kFull, x, j);
-      } else {
-        __syncthreads();
-        buf[t] = x;
-        __syncthreads();
-        y = buf[t ^ j];
-      }
-      const bool low = ((t & k) == 0) == ((t & j) == 0);
-      x = low ? min(x, y) : max(x, y);
+  while (true) {
+    const int shift = max(0, 64 - __clzll((hi - lo - 1) | 1) - 10);  // to kList bins
+    const bool here = in && x >= lo && x < hi;
+    number[t] = 0u;
+    if (kMass) mass[t] = 0ull;
+    if (t == 0) s.found[2] = 0;
+    __syncthreads();
+    if (here) {
+      const uint32_t b = uint32_t((x - lo) >> shift);
+      atomicAdd(&number[b], 1u);
+      if (kMass) atomicAdd(&mass[b], static_cast<unsigned long long>(w));
     }
+    __syncthreads();
+    const uint64_t mine = kMass ? uint64_t(mass[t]) : uint64_t(number[t]);
+    uint64_t upto = mine;
+    block_scan(s, upto);
+    upto += base;
+    if (upto - mine < target && upto >= target) {
+      s.found[0] = lo + (uint64_t(t) << shift);
+      s.found[1] = upto - mine;
+      s.found[2] = number[t];
+    }
+    __syncthreads();
+    const uint64_t n = s.found[2];
+    if (n == 0) return ~0ull;
+    lo = s.found[0];
+    hi = min(hi, lo + (uint64_t(1) << shift));
+    base = s.found[1];
+    if (n == 1 || shift == 0) break;
+    __syncthreads();
   }
-  return x;
+  if (in && x >= lo && x < hi) s.found[3] = x;
+  __syncthreads();
+  return s.found[3];
 }
 
 // A row's settings, and what it writes.
@@ -659,29 +682,30 @@ __device__ __forceinline__ void finish_few(Shared& s, const SampleParams& p, int
       write(p, row, int64_t(x[i] >> 32), weigh.log_part(value_of(uint32_t(x[i])), whole), kept);
 }
 
-// The same for more of them (at most kList), one per thread.  `whole`: the mass that top-p is of, if it is
-// known to be more than the list's.  False where top-p's cut lies behind the list.
+// The same for more of them (at most kList), one per thread; their places lie before `hi`.  `whole`: the mass
+// that top-p is of, if it is known to be more than the list's.  False where top-p's cut lies behind the list.
 __device__ __forceinline__ bool finish_list(Shared& s, const SampleParams& p, int64_t row, const Row& r,
-                                            const Weigh& weigh, uint32_t n, uint64_t whole) {
+                                            const Weigh& weigh, uint32_t n, uint64_t hi, uint64_t whole) {
   const uint32_t t = threadIdx.x;
-  uint64_t x = block_sort(s.buffer(), t < n ? s.list()[t] : ~0ull, n);
-  bool in = t < n && (r.k == 0 || t < r.k);
-  uint64_t w = in ? weigh(value_of(uint32_t(x >> 32))) : 0ull, upto = w;
-  const uint64_t listed = block_scan(s, upto);
+  const uint64_t lo = uint64_t(key_of(weigh.top)) << 32, x = t < n ? s.list()[t] : ~0ull;
+  const float z = value_of(uint32_t(x >> 32));
+  bool in = t < n;
+  if (r.k && r.k < n) {
+    const uint64_t cut = block_select<false>(s, x, in, 0, lo, hi, 0, r.k);  // by all threads: it has barriers
+    in = in && x <= cut;
+  }
+  uint64_t w = in ? weigh(z) : 0ull;
   if (r.nucleus) {
-    const uint64_t target = r.target(whole ? whole : listed);
+    const uint64_t listed = block_sums(s, warp_total(w)).all, target = r.target(whole ? whole : listed);
     if (listed < target) return false;
-    in = in && upto - w < target;
+    const uint64_t cut = block_select<true>(s, x, in, w, lo, hi, 0, target);
+    in = in && x <= cut;
   }
   in = in && w >= r.least;
   const uint32_t kept = __syncthreads_count(in);
-  x = block_sort(s.buffer(), in ? x << 32 | x >> 32 : ~0ull, kept);
-  in = t < kept;
-  const float z = value_of(uint32_t(x));
-  w = in ? weigh(z) : 0ull;
-  upto = w;
-  const uint64_t all = block_scan(s, upto), goal = r.goal(all);
-  if (upto > goal && upto - w <= goal) write(p, row, int64_t(x >> 32), weigh.log_part(z, all), kept);
+  const uint64_t all = block_sums(s, warp_total(in ? w : 0ull)).all, i = uint32_t(x);
+  const uint64_t drawn = block_select<true>(s, i, in, w, 0, uint64_t(p.vocab), 0, r.goal(all) + 1);
+  if (in && i == drawn) write(p, row, int64_t(i), weigh.log_part(z, all), kept);
   return true;
 }
 
@@ -943,7 +967,7 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
         if (few) {
           if (cl.rank == 0) {
             if (v.count + v.n > kFew) {
-              finish_list(s, p, row, r, weigh, v.count + v.n, 0);
+              finish_list(s, p, row, r, weigh, v.count + v.n, v.hi, 0);
             } else if (warp == 0) {
               finish_few(s, p, row, r, weigh, v.count + v.n);
             }
@@ -952,11 +976,9 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
         }
         uint64_t place = 0;
         if (cl.rank == 0) {
-          const uint64_t x = block_sort(s.buffer(), threadIdx.x < v.n ? s.list()[threadIdx.x] : ~0ull, v.n);
-          if (threadIdx.x == r.k - v.count - 1) s.found[0] = x;
+          const uint64_t x = threadIdx.x < v.n ? s.list()[threadIdx.x] : ~0ull;
+          place = block_select<false>(s, x, threadIdx.x < v.n, 0, v.lo, v.hi, v.count, r.k);
           if (threadIdx.x == 0) s.listed = 0u;
-          __syncthreads();
-          place = s.found[0];
         }
         cut_behind(cl.tell(place, 0)[0].a);
       } else {
@@ -1059,37 +1081,29 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
         target = r.target(whole);
         if (listing && few) {
           bool done = false;
-          if (cl.rank == 0) done = finish_list(s, p, row, r, weigh, through, whole);
+          if (cl.rank == 0) done = finish_list(s, p, row, r, weigh, through, v.hi, whole);
           if (cl.tell(done, 0)[0].a) return;
         } else if (listing) {
-          uint64_t place = 0, stays = 0;
+          uint64_t place = ~0ull, counts = 0;
           if (cl.rank == 0) {
             const uint32_t t = threadIdx.x, len = s.listed;
-            const uint64_t x = block_sort(s.buffer(), t < len ? s.list()[t] : ~0ull, len);
+            const uint64_t x = t < len ? s.list()[t] : ~0ull;
             const uint64_t w = t < len ? weigh(value_of(uint32_t(x >> 32))) : 0ull;
-            uint64_t at = w;
-            if (t == 0) s.found[0] = s.found[1] = 0;
-            block_scan(s, at);
-            s.list()[t] = x;
-            if (ahead + at - w < target && ahead + at >= target) {
-              s.found[0] = x;
-              s.found[1] = t + 1;
-            }
-            __syncthreads();
-            place = s.found[0];
-            stays = s.found[1];
+            if (ahead < target) place = block_select<true>(s, x, t < len, w, v.lo, v.hi, ahead, target);
+            counts = uint64_t(len) << 32 | uint32_t(__syncthreads_count(x <= place && t < len));
           }
-          const Pair* all = cl.tell(place, stays);
-          found = all[0].b != 0;
+          const Pair* all = cl.tell(place, counts);
+          place = all[0].a;
+          found = place != ~0ull;
           if (found) {
-            cut_behind(all[0].a);
+            cut_behind(place);
             listed = true;
             kept_n = before_lo + uint32_t(all[0].b);
             // what the listed entries that stay add to the warps in whose parts they lie
-            if (threadIdx.x < all[0].b) {
+            if (threadIdx.x < uint32_t(all[0].b >> 32)) {
               const uint64_t x = ld_cluster64(list_at + threadIdx.x * 8);
               const int j = int(uint32_t(x)) - sl.first;
-              if (j >= sl.lo && j < sl.hi)
+              if (x <= place && j >= sl.lo && j < sl.hi)
                 atomicAdd(reinterpret_cast<unsigned long long*>(&s.extra[j / sl.seg]),
                           static_cast<unsigned long long>(weigh(value_of(uint32_t(x >> 32)))));
             }
