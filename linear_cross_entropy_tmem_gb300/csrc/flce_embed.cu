@@ -67,10 +67,10 @@ __device__ __forceinline__ void store_elems(O* at, int count, const float (&x)[k
       if (e < count) at[e * kWide] = from_f32<O>(x[e]);
   }
 }
-// A block's columns [tile * blockDim.x * kElems, ...): the thread's first one, and how many it has.
+// Columns [tile * threads * kElems, ...) of `threads` threads: the t-th's first one, and how many it has.
 template <bool kVec>
-__device__ __forceinline__ int first_col(int tile, int cols, int& count) {
-  const int at = tile * int(blockDim.x) * kElems + int(threadIdx.x) * (kVec ? kElems : 1);
+__device__ __forceinline__ int first_col(int tile, int t, int threads, int cols, int& count) {
+  const int at = tile * threads * kElems + t * (kVec ? kElems : 1);
   count = at >= cols ? 0 : kVec ? kElems : min(kElems, (cols - at + kWide - 1) / kWide);
   return at;
 }
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedParams p) {
   const int tile = int(blockIdx.x % unsigned(p.tiles));
   const int64_t first = int64_t(blockIdx.x / unsigned(p.tiles)) * kRows;
   int cnt;
-  const int at = first_col<kVec>(tile, p.cols, cnt);
+  const int at = first_col<kVec>(tile, int(threadIdx.x), int(blockDim.x), p.cols, cnt);
   Raw<T> r[kRows];
   bool there[kRows];
 #pragma unroll
@@ -265,7 +265,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(SortParams
 // ---------------------------------------------------------------------------
 constexpr int kChunk = 32;             // sorted tokens of a block: a warp's worth of keys
 constexpr int kAhead = 4;              // rows under way at once
-constexpr int kZeroBytes = 128 << 10;  // of the table that a block clears
+constexpr int kMostTeams = 8;          // chunks of a block, where the rows are narrow
+constexpr int kZeroBytes = 128 << 10;  // of the table that a block clears, at most
+constexpr int kZeroLeast = 16 << 10;
 constexpr int kZeroRows = 4096;        // at most
 
 struct EmbedBwdParams {
@@ -275,7 +277,7 @@ struct EmbedBwdParams {
   float* part;        // [chunk][2][cols]: the run that enters a chunk, the run that leaves it
   uint32_t* joins;    // number of runs that cross a border, then the chunks in which they begin
   int64_t n, vocab, ds, ws;
-  int32_t cols, tiles, chunks, zero_rows;
+  int32_t cols, tiles, chunks, zero_rows, team;  // threads of a chunk
   float scale;
   int32_t accumulate;
 };
@@ -330,43 +332,49 @@ __device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, int64_t r0, 
     }
   }
   __syncthreads();
-  // a warp per row: single elements up to a 16-byte boundary, whole vectors, the rest
+  // a warp or a part of it per row: single elements up to a 16-byte boundary, whole vectors, the rest
   constexpr int kV = 16 / sizeof(O);
   const O zero = from_f32<O>(0.f);
-  for (int r = warp; r < rows; r += warps) {
+  const int lanes = p.cols > 16 * kV ? 32 : p.cols > 8 * kV ? 16 : 8, at = int(threadIdx.x) % lanes;
+  for (int r = int(threadIdx.x) / lanes; r < rows; r += int(blockDim.x) / lanes) {
     if ((named[r >> 5] >> (r & 31)) & 1u) continue;
     O* row = static_cast<O*>(p.dweight) + (r0 + r) * p.ws;
     const int head = min(p.cols, int((kV - (reinterpret_cast<uintptr_t>(row) / sizeof(O)) % kV) % kV));
     const int vecs = (p.cols - head) / kV, tail = head + vecs * kV;
-    if (lane < head) row[lane] = zero;
-    for (int i = lane; i < vecs; i += 32) *reinterpret_cast<uint4*>(row + head + i * kV) = make_uint4(0u, 0u, 0u, 0u);
-    if (tail + lane < p.cols) row[tail + lane] = zero;
+    if (at < head) row[at] = zero;
+    for (int i = at; i < vecs; i += lanes) *reinterpret_cast<uint4*>(row + head + i * kV) = make_uint4(0u, 0u, 0u, 0u);
+    if (tail + at < p.cols) row[tail + at] = zero;
   }
 }
 
 template <class T, class O, bool kVec>
 __global__ void __launch_bounds__(256, 3) embed_sum_kernel(EmbedBwdParams p) {
   __shared__ uint32_t named[kZeroRows / 32];
-  __shared__ uint32_t keys[2 * kChunk + 2];
-  __shared__ uint32_t tokens[2 * kChunk];
-  __shared__ int range[4];
+  __shared__ uint32_t all_keys[kMostTeams][2 * kChunk + 2];
+  __shared__ uint32_t all_tokens[kMostTeams][2 * kChunk];
+  __shared__ int ranges[kMostTeams][4];
   griddep_wait();  // the tokens are sorted
   griddep_release();
-  const int64_t sums = int64_t(p.chunks) * p.tiles;
+  const int teams = int(blockDim.x) / p.team;
+  const int64_t sums = cdiv(p.chunks, teams) * p.tiles;
   if (int64_t(blockIdx.x) >= sums) {
     const int64_t r0 = (int64_t(blockIdx.x) - sums) * p.zero_rows;
     clear_rows<O>(p, r0, min(p.vocab, r0 + p.zero_rows), named);
     return;
   }
+  const int team = int(threadIdx.x) / p.team, t = int(threadIdx.x) % p.team;
+  uint32_t* keys = all_keys[team];
+  uint32_t* tokens = all_tokens[team];
+  int* range = ranges[team];
   const int tile = int(blockIdx.x % unsigned(p.tiles));
-  const int chunk = int(blockIdx.x / unsigned(p.tiles));
+  const int chunk = int(blockIdx.x / unsigned(p.tiles)) * teams + team;  // behind the last one: no tokens
   const int64_t begin = int64_t(chunk) * kChunk;
   int count;
-  const int at = first_col<kVec>(tile, p.cols, count);
+  const int at = first_col<kVec>(tile, t, p.team, p.cols, count);
   const T* dout = static_cast<const T*>(p.dout) + at;
-  if (threadIdx.x < 32) {
+  if (t < 32) {
     // keys[1 + j] is the chunk's j-th, those of the next one behind them; before and after them, their neighbours
-    const int lane = int(threadIdx.x);
+    const int lane = t;
     auto entry = [&](int64_t i) { return i >= 0 && i < p.n ? p.sorted[i] : ~0ull; };
     const uint64_t e0 = entry(begin + lane), e1 = entry(begin + kChunk + lane);
     const uint32_t k0 = key_of(e0), k1 = key_of(e1);
@@ -428,7 +436,7 @@ __global__ void __launch_bounds__(256, 3) embed_sum_kernel(EmbedBwdParams p) {
       if (j == enters || j == leaves) {
         const bool out = j != enters;
         store_elems<float, kVec>(part + (out ? p.cols : 0) + at, count, acc);
-        if (out && tile == 0 && threadIdx.x == 0) p.joins[1 + atomicAdd(p.joins, 1u)] = uint32_t(chunk);
+        if (out && tile == 0 && t == 0) p.joins[1 + atomicAdd(p.joins, 1u)] = uint32_t(chunk);
       } else {
         write_row<O, kVec>(p, key, at, count, acc);
       }
@@ -557,8 +565,12 @@ template <class T, class O, bool kVec>
 cudaError_t launch_sum(EmbedBwdParams& q, cudaStream_t st) {
   const int threads = row_threads(q.cols, kVec);
   q.tiles = int32_t(cdiv(q.cols, int64_t(threads) * kElems));
+  // blocks of 160 threads or more: narrow rows have several chunks in one
+  const int teams = 256 / threads;
+  q.team = threads;
   const int64_t clear = q.accumulate ? 0 : cdiv(q.vocab, q.zero_rows);
-  return launch_dependent(embed_sum_kernel<T, O, kVec>, unsigned(int64_t(q.chunks) * q.tiles + clear), threads, st, q);
+  return launch_dependent(embed_sum_kernel<T, O, kVec>, unsigned(cdiv(q.chunks, teams) * q.tiles + clear),
+                          teams * threads, st, q);
 }
 template <class T, class O>
 cudaError_t launch_sum(EmbedBwdParams& q, cudaStream_t st) {
@@ -659,7 +671,10 @@ int flce_embedding_backward(const flce_embedding_problem* problem, const void* i
   q.ws = p->weight_stride;
   q.cols = int32_t(p->cols);
   q.chunks = int32_t(cdiv(p->tokens, kChunk));
-  q.zero_rows = int32_t(std::max<int64_t>(1, std::min<int64_t>(kZeroRows, kZeroBytes / (p->cols * elem_size(p->weight_dtype)))));
+  // eight blocks to an SM clear the table, if that makes enough for each
+  const int64_t row_bytes = p->cols * int64_t(elem_size(p->weight_dtype));
+  const int64_t clear = std::clamp<int64_t>(p->vocab * row_bytes / (int64_t(dev.num_sms) * 8), kZeroLeast, kZeroBytes);
+  q.zero_rows = int32_t(std::clamp<int64_t>(clear / row_bytes, 1, kZeroRows));
   q.scale = p->scale;
   q.accumulate = p->accumulate;
   FLCE_TRY(logged(FLCE_LAUNCH_OTHER, st, [&] {
