@@ -70,45 +70,25 @@ __device__ __forceinline__ void quantize_adjacent(float (&y)[8], bool write, uin
   w |= __shfl_xor_sync(kFull, w, 4);
   word = w | __shfl_xor_sync(kFull, w, 8);
 }
-// The same where a lane has one column of each of eight blocks; `to` is the segment's first byte.
-__device__ __forceinline__ void quantize_apart(float (&y)[8], uint32_t blocks, uint8_t* to, uint32_t& word) {
-  const int lane = threadIdx.x & 31;
-  uint32_t w[2] = {0u, 0u}, bad = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t top = __reduce_max_sync(kFull, __float_as_uint(y[e]) & 0x7fffffffu);
-    const uint32_t s = scale_byte(top);
-    y[e] *= inverse_scale(s);
-    bad |= s == 255u ? 15u << (4 * e) : 0u;
-    w[e >> 2] |= s << (8 * (e & 3));
-  }
-  word = lane < 16 ? w[0] : w[1];
-  const uint32_t nibbles = to_e2m1x8(y) & ~bad;  // of block e at bits 4 e
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    uint32_t v = ((nibbles >> (4 * e)) & 15u) << (4 * (lane & 7));
-    v |= __shfl_xor_sync(kFull, v, 1);
-    v |= __shfl_xor_sync(kFull, v, 2);
-    v |= __shfl_xor_sync(kFull, v, 4);
-    if ((lane & 7) == 0 && e < int(blocks)) *reinterpret_cast<uint32_t*>(to + e * 16 + (lane >> 3) * 4) = v;
-  }
-}
-
 __device__ __forceinline__ void copy_async16(void* dst, const void* src, int bytes) {  // the rest of 16 as zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
 }
 
 // kVec: rows start on 16-byte boundaries.  A warp keeps the rows of kItems - 1 further
 // items under way, copied into shared memory of its own (each lane reads what it
-// copied).  128256 x 2048 bf16, where
-// the copy rate gives 98 us: 137 us; with loads to registers, 80 KB of them under way
-// on an SM, 170.
+// copied).  128256 x 2048 bf16, where the copy rate gives 98 us: 137 us; with loads to
+// registers, 80 KB of them under way on an SM, 170.
+// Else the warp loads 32 adjacent elements at a time and passes them on through shared
+// memory: 1380 x 9469 bf16 9.4 us, the copy rate gives 4.9.  (Asynchronous copies of 4
+// or 8 bytes where rows start on such: 20000 x 1027 fp32 36 us in place of 20, 28992 x
+// 396 fp16 10.7 in place of 10.1.)
 template <class T>
 constexpr int kItems = sizeof(T) == 2 ? 4 : 2;
 template <class T>
 constexpr int kItemBytes = 4 * 32 * 8 * int(sizeof(T));
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kThreadsQ) mx_quantize_kernel(MxQuantParams p) {
+  constexpr int kSlots = kVec ? kItems<T> : 1;
   extern __shared__ __align__(16) uint8_t ring[];
   griddep_release();
   if (p.status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
@@ -120,7 +100,7 @@ __global__ void __launch_bounds__(kThreadsQ) mx_quantize_kernel(MxQuantParams p)
     r0 = it.tile * p.tile_rows + it.half * 128 + it.r32;
     return int(min((min(int64_t(p.tile_rows) * (it.tile + 1), p.rows) - r0 + 31) / 32, int64_t(4)));
   };
-  Vec<T, 8>* mine = reinterpret_cast<Vec<T, 8>*>(ring) + warp * kItems<T> * 128 + lane;  // [item][row][lane]
+  Vec<T, 8>* mine = reinterpret_cast<Vec<T, 8>*>(ring) + warp * kSlots * 128 + lane;  // [item][row][lane]
   auto copy = [&](int64_t item, int slot) {
     if (item < p.items) {
       const Item it(item, p.segs, p.halves);
@@ -132,16 +112,17 @@ __global__ void __launch_bounds__(kThreadsQ) mx_quantize_kernel(MxQuantParams p)
       for (int i = 0; i < 4; ++i, row += 32 * p.stride) {
         const int n = i < rows ? bytes : 0;
         uint8_t* dst = reinterpret_cast<uint8_t*>(mine + slot * 128 + i * 32);
-        const uint8_t* src = n > 0 ? reinterpret_cast<const uint8_t*>(row) : static_cast<const uint8_t*>(p.x);
-        copy_async16(dst, src, min(n, 16));
-        if (sizeof(T) == 4) copy_async16(dst + 16, n > 16 ? src + 16 : static_cast<const uint8_t*>(p.x), max(n - 16, 0));
+#pragma unroll
+        for (int o = 0; o < 8 * int(sizeof(T)); o += 16)
+          copy_async16(dst + o, n > o ? reinterpret_cast<const uint8_t*>(row) + o : static_cast<const uint8_t*>(p.x),
+                            max(0, min(n - o, 16)));
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   if constexpr (kVec) {
 #pragma unroll
-    for (int k = 0; k < kItems<T> - 1; ++k) copy(first + k * step, k);
+    for (int k = 0; k < kSlots - 1; ++k) copy(first + k * step, k);
   }
   int slot = 0;
   for (int64_t item = first; item < p.items; item += step) {
@@ -150,36 +131,35 @@ __global__ void __launch_bounds__(kThreadsQ) mx_quantize_kernel(MxQuantParams p)
     int64_t r0;
     const int rows = rows_of(it, r0);
     if constexpr (kVec) {
-      copy(item + (kItems<T> - 1) * step, (slot + kItems<T> - 1) % kItems<T>);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kItems<T> - 1) : "memory");
-    }
-    Vec<T, 8> apart[kVec ? 1 : 4];
-    if constexpr (!kVec) {
+      copy(item + (kSlots - 1) * step, (slot + kSlots - 1) % kSlots);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
+    } else {
+      T x[4][8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const T* row = static_cast<const T*>(p.x) + (r0 + 32 * i) * p.stride;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int c = col0 + e * 32 + lane;
-          apart[i].v[e] = i < rows && c < p.cols ? row[c] : from_f32<T>(0.f);
+          x[i][e] = i < rows && c < p.cols ? row[c] : from_f32<T>(0.f);
         }
       }
+      __syncwarp();  // the last item's are read
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) reinterpret_cast<T*>(mine - lane + i * 32)[e * 32 + lane] = x[i][e];
+      __syncwarp();
     }
     uint32_t word[4];  // the scale bytes of the row's four blocks of the lane's group
     uint8_t* to = p.codes + r0 * row_bytes + col0 / 2;
 #pragma unroll
     for (int i = 0; i < 4; ++i, to += int64_t(32) * row_bytes) {
       float y[8];
-      if constexpr (kVec) {
-        const Vec<T, 8> x = mine[slot * 128 + i * 32];
+      const Vec<T, 8> x = mine[slot * 128 + i * 32];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = to_f32(x.v[e]);
-        quantize_adjacent(y, i < rows && col0 + (lane & ~3) * 8 < p.cols, reinterpret_cast<uint32_t*>(to) + lane, word[i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = to_f32(apart[i].v[e]);
-        quantize_apart(y, i < rows ? uint32_t(p.cols - col0 + 31) / 32 : 0u, to, word[i]);
-      }
+      for (int e = 0; e < 8; ++e) y[e] = to_f32(x.v[e]);
+      quantize_adjacent(y, i < rows && col0 + (lane & ~3) * 8 < p.cols, reinterpret_cast<uint32_t*>(to) + lane, word[i]);
     }
     // a group's tile: 16 bytes for r32, four for each of the rows
     const int group = it.seg * 2 + (lane >> 4);
@@ -187,7 +167,7 @@ __global__ void __launch_bounds__(kThreadsQ) mx_quantize_kernel(MxQuantParams p)
       uint8_t* t = p.scales + ((it.tile * p.groups + group) * p.halves + it.half) * kScaleTile + it.r32 * 16;
       *reinterpret_cast<uint4*>(t) = make_uint4(word[0], word[1], word[2], word[3]);
     }
-    slot = (slot + 1) % kItems<T>;
+    slot = (slot + 1) % kSlots;
   }
 }
 
@@ -207,22 +187,28 @@ struct MxDequantParams {
   int32_t cols, groups, segs;
 };
 
-// The same warps' work as above; a lane has eight adjacent columns.
+// The same warps' work as above; a lane has eight adjacent columns.  kVec: the rows
+// start on 16-byte boundaries; else the warp passes each row on through shared memory
+// and stores 32 adjacent elements at a time (1380 x 9469 bf16: 7.4 us,
+// the copy rate gives 4.9; with each lane's own elements stored one by one, 40).
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kThreadsQ) mx_dequantize_kernel(MxDequantParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * kWarpsQ + (threadIdx.x >> 5);
+  __shared__ __align__(16) T turned[kVec ? 1 : kWarpsQ][kVec ? 8 : kSeg];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t item = int64_t(blockIdx.x) * kWarpsQ + warp;
   if (item >= p.items) return;
   const Item it(item, p.segs, 1);
   const int c = it.seg * kSeg + lane * 8, group = it.seg * 2 + (lane >> 4);
-  if (c >= p.cols) return;
+  const bool in = c < p.cols;
+  if (kVec && !in) return;
   const int64_t row_bytes = mx_cdiv(p.cols, kMxBlock) * 16, r0 = it.tile * 128 + it.r32;
-  const uint4 s4 = *reinterpret_cast<const uint4*>(p.scales + (it.tile * p.groups + group) * kScaleTile + it.r32 * 16);
+  uint4 s4 = make_uint4(0u, 0u, 0u, 0u);
+  if (in) s4 = *reinterpret_cast<const uint4*>(p.scales + (it.tile * p.groups + group) * kScaleTile + it.r32 * 16);
   const uint32_t words[4] = {s4.x, s4.y, s4.z, s4.w};
   uint32_t codes[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (r0 + 32 * i < p.rows) codes[i] = *reinterpret_cast<const uint32_t*>(p.codes + (r0 + 32 * i) * row_bytes + c / 2);
+    codes[i] = in && r0 + 32 * i < p.rows ? *reinterpret_cast<const uint32_t*>(p.codes + (r0 + 32 * i) * row_bytes + c / 2) : 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t r = r0 + 32 * i;
@@ -236,12 +222,23 @@ __global__ void __launch_bounds__(kThreadsQ) mx_dequantize_kernel(MxDequantParam
       v.v[2 * e + 1] = from_f32<T>(x.y * scale);
     }
     T* row = static_cast<T*>(p.out) + r * p.stride;
-    if (kVec && c + 8 <= p.cols) {
-      store_vec<T, 8>(row + c, v);
-    } else {
+    if constexpr (kVec) {
+      if (c + 8 <= p.cols) {
+        store_vec<T, 8>(row + c, v);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < p.cols) row[c + e] = v.v[e];
+        for (int e = 0; e < 8; ++e)
+          if (c + e < p.cols) row[c + e] = v.v[e];
+      }
+    } else {
+      __syncwarp();  // the last row's are read
+      store_vec<T, 8>(&turned[warp][lane * 8], v);
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int col = it.seg * kSeg + e * 32 + lane;
+        if (col < p.cols) row[col] = turned[warp][e * 32 + lane];
+      }
     }
   }
 }
@@ -250,19 +247,20 @@ bool whole_rows(const void* p, int64_t stride, int64_t rows, size_t es) {
   return aligned_to(p, 16) && (rows <= 1 || stride * int64_t(es) % 16 == 0);
 }
 
+template <class T, bool kVec>
+cudaError_t launch_quantize(const MxQuantParams& p, int num_sms, cudaStream_t st) {
+  auto kern = mx_quantize_kernel<T, kVec>;
+  constexpr int smem = kWarpsQ * (kVec ? kItems<T> : 1) * kItemBytes<T>;  // kVec: three blocks on an SM
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = std::min<int64_t>(mx_cdiv(p.items, kWarpsQ), int64_t(num_sms) * (kVec ? 3 : 32));
+  kern<<<unsigned(grid), kThreadsQ, smem, st>>>(p);
+  return cudaGetLastError();
+}
 template <class T>
 cudaError_t launch_quantize(const MxQuantParams& p, int num_sms, cudaStream_t st) {
-  const int64_t want = mx_cdiv(p.items, kWarpsQ);
-  if (whole_rows(p.x, p.stride, p.rows, sizeof(T))) {
-    auto kern = mx_quantize_kernel<T, true>;
-    constexpr int smem = kWarpsQ * kItems<T> * kItemBytes<T>;  // three blocks on an SM
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    kern<<<unsigned(std::min<int64_t>(want, int64_t(num_sms) * 3)), kThreadsQ, smem, st>>>(p);
-  } else {
-    mx_quantize_kernel<T, false><<<unsigned(std::min<int64_t>(want, int64_t(num_sms) * 32)), kThreadsQ, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  return whole_rows(p.x, p.stride, p.rows, sizeof(T)) ? launch_quantize<T, true>(p, num_sms, st)
+                                                      : launch_quantize<T, false>(p, num_sms, st);
 }
 template <class T>
 cudaError_t launch_dequantize(const MxDequantParams& p, cudaStream_t st) {
