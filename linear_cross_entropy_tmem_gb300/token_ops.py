@@ -137,7 +137,10 @@ class Embedding(torch.autograd.Function):
 def embedding(weight: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, padding_idx: Optional[int] = None,
               out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """``weight[ids] * scale`` with the table's gradient: rows of ids outside [0, V) are zeros, and neither they nor
-    ``padding_idx`` have one."""
+    ``padding_idx`` have one.
+
+    A backward captured into a CUDA graph: while an earlier graph of the same leaf lives, autograd adds to the leaf on
+    the stream on which that graph was recorded.  Record it on the capturing stream, or drop it before the capture."""
     return Embedding.apply(weight, ids, float(scale), padding_idx, out_dtype)
 
 
