@@ -6,14 +6,14 @@
 // Few tokens: bound by the weight's bytes, 17/32 of V D.  The weight is the MMA's
 // A operand (128 vocabulary entries, TMEM lanes), the tokens its B operand (16 to
 // 208 TMEM columns), so that a single token costs a tile of 16 columns and not of
-// 128 rows.  4096 x 151936: 55 us for one token (the bytes alone 49), 60 for 64, 76 for
+// 128 rows.  4096 x 151936: 55 us for one token (the bytes alone 49), 59 for 64, 73 for
 // 208.
 //
-// Many tokens: bound by what the tiles take from L2, 43 KB for 128 x 192 x 256, or
-// rather by the bytes under way (five stages) over the 1.7 us that a stage takes
-// around its loop: 2047 tokens take 522 us, 4.9 PFLOP/s.  (CTA pairs with tiles of
-// 256 x 192 take less from L2, but had as many bytes under way and a longer loop:
-// 553 us.)
+// Many tokens: 2047 take 490 us, 5.2 PFLOP/s.  What a tile takes from L2 (43 KB for 128 x
+// 192 x 256) takes 335 us by itself; the products, which run under it, add 20, the copies of
+// the scales, in line with them, 60, the epilogue's work on TMEM and its stores 70.  (CTA
+// pairs with tiles of 256 x 192 take a third less from L2, but the loads alone took them
+// longer, also with seven stages under way: 550 and 633 us.)
 //
 //   warp 8     TMA producer: per stage 256 columns (128 bytes of a row, one
 //              swizzle atom) of both operands, and their scales as they lie in
@@ -44,6 +44,8 @@ constexpr int kMxRow = kMxK / 2;       // bytes
 constexpr int kMxMaxStages = 10;
 constexpr int kMxSmem = 216 << 10;     // for the stages
 constexpr uint32_t kTmemAll = 512;
+constexpr int kMxTurn = 4096;          // bytes in which an epilogue group turns its output round
+constexpr int kMxTurnTokens = 17;      // from so many tokens on (8 tokens: 58.4 us either way)
 
 struct MxLogitsParams {
   const uint8_t *a_scales, *b_scales;
@@ -74,7 +76,7 @@ __device__ __forceinline__ uint32_t instr_desc_mxf4(uint32_t n, uint32_t half) {
 // control flow is uniform the descriptors stay in uniform registers.  (Issued from one
 // thread's own branch, a stage's four copies and four MMAs took 600 cycles, more than
 // the stage's bytes: one token of 4096 x 151936 took 63 us in place of 55, 2047 tokens 676 in
-// place of 522.)
+// place of 522 at the time.)
 __device__ __forceinline__ void umma_mxf4(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t accumulate) {
   asm volatile(
@@ -121,11 +123,13 @@ __device__ __forceinline__ float tanh_both(float u) {
   return u != u ? u : y;  // (the bounds of t would hide a NaN)
 }
 
+constexpr int kMxBarrierBytes = 1024;
 struct MxSmem {
   uint8_t* stage;
   uint64_t *full, *empty, *tfull, *tempty, *drain;
   uint32_t* tmem_slot;
   CtaControl* ctl;
+  uint8_t* turn;
 };
 __device__ __forceinline__ MxSmem carve(uint8_t* raw, int stages, int stage_bytes) {
   MxSmem s;
@@ -137,9 +141,9 @@ __device__ __forceinline__ MxSmem carve(uint8_t* raw, int stages, int stage_byte
   s.drain = s.tempty + kAccBufs;
   s.tmem_slot = reinterpret_cast<uint32_t*>(s.drain + 1);
   s.ctl = reinterpret_cast<CtaControl*>(s.tmem_slot + 2);
+  s.turn = s.stage + stages * stage_bytes + kMxBarrierBytes;
   return s;
 }
-constexpr int kMxBarrierBytes = 1024;
 
 // As mbar_wait, but the clock and the abort flag are looked at once in 64 tries: these waits end within a
 // microsecond, and their wake-up is on the way of every stage.
@@ -165,6 +169,21 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, CtaCon
   const uint32_t addr = smem_u32(bar);
   if (__all_sync(0xffffffffu, mbar_try_wait(addr, parity))) return true;
   return __all_sync(0xffffffffu, stage_wait(bar, parity, ctl, status));
+}
+
+// The four warps of an epilogue group.
+__device__ __forceinline__ void group_sync(int grp) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + grp) : "memory");
+}
+__device__ __forceinline__ bool group_all(int grp, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(all)
+      : "r"(uint32_t(ok)), "r"(1 + grp)
+      : "memory");
+  return all != 0;
 }
 
 // Until a copy or an MMA that this thread started has ended (bounded all the same).
@@ -199,7 +218,11 @@ struct Step {
   }
 };
 
-template <class O>
+// kTurned: rows of the output start on 16-byte boundaries.  TMEM's lanes are vocabulary entries, so
+// that a warp has 32 of a token's logits; the group's four warps turn 128 of several tokens' round in
+// shared memory, and store lines of 256 or 512 bytes (2047 tokens 490 us in place of 522 with
+// 64 bytes from a warp; 64 tokens to fp32, 128256 x 2048, 34 in place of 37).
+template <class O, bool kTurned>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_logits_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                      const __grid_constant__ MxLogitsParams p, int* status) {
@@ -343,25 +366,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     int seq = 0;
     for (int u = first; u < units; u += stride, ++seq) {
       if ((seq & 1) != grp) continue;
-      if (!stage_wait(&sm.tfull[grp], phase, sm.ctl, status)) break;
+      bool ok = stage_wait(&sm.tfull[grp], phase, sm.ctl, status);
+      if constexpr (kTurned) ok = group_all(grp, ok);  // (they give up as one)
+      if (!ok) break;
       tc_fence_after();
       int m, n;
       tile_of(p, u, m, n);
-      const int v = m * kMxM + quarter * 32 + int(lane_id());
+      const int v0 = m * kMxM, v = v0 + quarter * 32 + int(lane_id());
       const float bias = p.bias && v < p.vocab ? load_as(p.bias, p.bias_dtype, v) : 0.f;
       const int n0 = n * p.tile_n, count = min(p.tile_n, p.tokens - n0);
-      O* out = static_cast<O*>(p.out) + int64_t(n0) * p.os + v;
+      O* out0 = static_cast<O*>(p.out) + int64_t(n0) * p.os + v0;
       for (int c = 0; c < count; c += 32) {
         uint32_t r[32];
         tmem_ld32(taddr + uint32_t(c), r);
         tmem_ld_wait(r);
+        auto logit = [&](int j) {
+          float z = (__uint_as_float(r[j]) + bias) * p.scale;
+          if (p.cap > 0.f) z = p.cap * tanh_both(z * p.inv_cap);
+          return from_f32<O>(z);
+        };
+        if constexpr (kTurned) {
+          constexpr int kRows = kMxTurn / (kMxM * int(sizeof(O))), kE = 16 / int(sizeof(O)), kPerRow = kMxM / kE;
+          O* turn = reinterpret_cast<O*>(sm.turn + grp * kMxTurn);
+          const int t = quarter * 32 + int(lane_id());
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (c + j < count && v < p.vocab) {
-            float z = (__uint_as_float(r[j]) + bias) * p.scale;
-            if (p.cap > 0.f) z = p.cap * tanh_both(z * p.inv_cap);
-            out[int64_t(c + j) * p.os] = from_f32<O>(z);
+          for (int k = 0; k < 32; k += kRows) {
+            if (c + k >= count) break;
+            group_sync(grp);  // the rows before are read
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) turn[j * kMxM + t] = logit(k + j);
+            group_sync(grp);
+#pragma unroll
+            for (int i = t; i < kRows * kPerRow; i += 128) {
+              const int row = c + k + i / kPerRow, at = i % kPerRow * kE;
+              if (row >= count) break;
+              const Vec<O, kE> x = load_vec<O, kE>(turn + i * kE);
+              O* to = out0 + int64_t(row) * p.os + at;
+              if (v0 + at + kE <= p.vocab) {
+                store_vec<O, kE>(to, x);
+              } else {
+#pragma unroll
+                for (int e = 0; e < kE; ++e)
+                  if (v0 + at + e < p.vocab) to[e] = x.v[e];
+              }
+            }
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c + j < count && v < p.vocab) out0[int64_t(c + j) * p.os + (v - v0)] = logit(j);
         }
       }
       tc_fence_before();
@@ -415,13 +468,13 @@ int validate(const flce_mxfp4_logits_problem* p) {
   return FLCE_OK;
 }
 
-template <class O>
+template <class O, bool kTurned>
 cudaError_t launch_logits(const CUtensorMap& a, const CUtensorMap& b, const MxLogitsParams& q, int* status, int num_sms,
                           cudaStream_t st) {
-  auto kern = mx_logits_kernel<O>;
-  const int smem = 1024 + q.stages * q.stage_bytes + kMxBarrierBytes;
+  auto kern = mx_logits_kernel<O, kTurned>;
+  const int smem = 1024 + q.stages * q.stage_bytes + kMxBarrierBytes + 2 * kMxTurn;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             1024 + kMxSmem + kMxBarrierBytes);
+                                             1024 + kMxSmem + kMxBarrierBytes + 2 * kMxTurn);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -434,6 +487,13 @@ cudaError_t launch_logits(const CUtensorMap& a, const CUtensorMap& b, const MxLo
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, a, b, q, status);
+}
+template <class O>
+cudaError_t launch_logits(const CUtensorMap& a, const CUtensorMap& b, const MxLogitsParams& q, int* status, int num_sms,
+                          cudaStream_t st) {
+  const bool lines = q.tokens >= kMxTurnTokens && aligned_to(q.out, 16) && q.os * int64_t(sizeof(O)) % 16 == 0;
+  return lines ? launch_logits<O, true>(a, b, q, status, num_sms, st)
+               : launch_logits<O, false>(a, b, q, status, num_sms, st);
 }
 
 }  // namespace
