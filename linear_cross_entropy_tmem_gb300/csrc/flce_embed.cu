@@ -297,16 +297,13 @@ __device__ __forceinline__ int64_t lower_bound(const uint64_t* sorted, int64_t l
   return lo;
 }
 
-template <class O, bool kVec>
-__device__ __forceinline__ void write_row(const EmbedBwdParams& p, uint32_t id, int at, int count,
-                                          const float (&acc)[kElems]) {
-  O* to = static_cast<O*>(p.dweight) + int64_t(id) * p.ws + at;
+// kAdd: to what the row has, `old`.
+template <class O, bool kVec, bool kAdd>
+__device__ __forceinline__ void write_row(O* to, float scale, int count, const float (&acc)[kElems], const Raw<O>& old) {
   float x[kElems];
 #pragma unroll
-  for (int e = 0; e < kElems; ++e) x[e] = __fmul_rn(acc[e], p.scale);
-  if (p.accumulate) {
-    Raw<O> old;
-    load_elems<O, kVec>(to, count, old);
+  for (int e = 0; e < kElems; ++e) x[e] = __fmul_rn(acc[e], scale);
+  if constexpr (kAdd) {
 #pragma unroll
     for (int e = 0; e < kElems; ++e) x[e] = __fadd_rn(to_f32(old.v.v[e]), x[e]);
   }
@@ -347,8 +344,10 @@ __device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, int64_t r0, 
   }
 }
 
-template <class T, class O, bool kVec>
-__global__ void __launch_bounds__(256, 3) embed_sum_kernel(EmbedBwdParams p) {
+// kAdd: the sums are added to the table's rows, which are loaded with those of the tokens (28 tokens into 118528 x 64
+// bf16: 21.6 us, 16384 into 151936 x 4096 fp32 124; loaded one by one as their sums end, 24 and 136).
+template <class T, class O, bool kVec, bool kAdd>
+__global__ void __launch_bounds__(256, kAdd ? 2 : 3) embed_sum_kernel(EmbedBwdParams p) {
   __shared__ uint32_t named[kZeroRows / 32];
   __shared__ uint32_t all_keys[kMostTeams][2 * kChunk + 2];
   __shared__ uint32_t all_tokens[kMostTeams][2 * kChunk];
@@ -372,6 +371,7 @@ __global__ void __launch_bounds__(256, 3) embed_sum_kernel(EmbedBwdParams p) {
   int count;
   const int at = first_col<kVec>(tile, t, p.team, p.cols, count);
   const T* dout = static_cast<const T*>(p.dout) + at;
+  O* dweight = static_cast<O*>(p.dweight) + at;
   if (t < 32) {
     // keys[1 + j] is the chunk's j-th, those of the next one behind them; before and after them, their neighbours
     const int lane = t;
@@ -419,10 +419,16 @@ __global__ void __launch_bounds__(256, 3) embed_sum_kernel(EmbedBwdParams p) {
   for (int j0 = range[0]; j0 < end; j0 += kAhead) {
     if (keys[1 + j0] >= none) break;
     Raw<T> r[kAhead];
+    Raw<O> old[kAdd ? kAhead : 1];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (j0 + u < end && keys[1 + j0 + u] < none)
-        load_elems<T, kVec>(dout + int64_t(tokens[j0 + u]) * p.ds, count, r[u]);
+    for (int u = 0; u < kAhead; ++u) {
+      const int j = j0 + u;
+      if (j >= end || keys[1 + j] >= none) break;
+      load_elems<T, kVec>(dout + int64_t(tokens[j]) * p.ds, count, r[u]);
+      if constexpr (kAdd)
+        if ((keys[2 + j] != keys[1 + j] || j + 1 == end) && j != enters && j != leaves)
+          load_elems<O, kVec>(dweight + int64_t(keys[1 + j]) * p.ws, count, old[u]);
+    }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int j = j0 + u;
@@ -438,7 +444,7 @@ __global__ void __launch_bounds__(256, 3) embed_sum_kernel(EmbedBwdParams p) {
         store_elems<float, kVec>(part + (out ? p.cols : 0) + at, count, acc);
         if (out && tile == 0 && t == 0) p.joins[1 + atomicAdd(p.joins, 1u)] = uint32_t(chunk);
       } else {
-        write_row<O, kVec>(p, key, at, count, acc);
+        write_row<O, kVec, kAdd>(dweight + int64_t(key) * p.ws, p.scale, count, acc, old[kAdd ? u : 0]);
       }
 #pragma unroll
       for (int e = 0; e < kElems; ++e) acc[e] = 0.f;
@@ -569,8 +575,9 @@ cudaError_t launch_sum(EmbedBwdParams& q, cudaStream_t st) {
   const int teams = 256 / threads;
   q.team = threads;
   const int64_t clear = q.accumulate ? 0 : cdiv(q.vocab, q.zero_rows);
-  return launch_dependent(embed_sum_kernel<T, O, kVec>, unsigned(cdiv(q.chunks, teams) * q.tiles + clear),
-                          teams * threads, st, q);
+  const unsigned grid = unsigned(cdiv(q.chunks, teams) * q.tiles + clear);
+  return q.accumulate ? launch_dependent(embed_sum_kernel<T, O, kVec, true>, grid, teams * threads, st, q)
+                      : launch_dependent(embed_sum_kernel<T, O, kVec, false>, grid, teams * threads, st, q);
 }
 template <class T, class O>
 cudaError_t launch_sum(EmbedBwdParams& q, cudaStream_t st) {
