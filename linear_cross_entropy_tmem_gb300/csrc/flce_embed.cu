@@ -8,13 +8,17 @@
 // gradient reads one per token and writes the whole table.
 //
 // The gradient has three launches.  One cluster sorts the tokens by id (stable,
-// so equal ids stay in the tokens' order).  Then blocks of kChunk sorted tokens
-// sum their rows in registers.  A run of one id that ends in its chunk or the one
-// behind it is the first one's block's, and goes straight to the table; the parts
-// of longer runs go to fp32 slots.  Other blocks of the same launch write zeros to
-// the rows that no token names, so that every row is written once.  The third
-// launch joins the parts, in order.  Nothing depends on the order in which blocks
-// run: same bits every time.
+// so equal ids stay in the tokens' order; 16 us for 16384), while the other SMs clear
+// the table's last rows.  Then blocks of kChunk sorted tokens sum their rows in
+// registers.  A run of one id that ends in its chunk or the one behind it is the first
+// one's block's, and goes straight to the table; the parts of longer runs go to fp32
+// slots.  Other blocks of the same launch write zeros to those of the other rows that
+// no token names, so that these are written once.  The third launch joins the parts,
+// in order.  Nothing depends on the order in which blocks run: same bits every time.
+//
+// 16384 x 4096 bf16 over 151936 rows: lookup 63 us (the copy rate gives 59), gradient
+// 225 (203).  8 rows: 1.9.  4099 x 1283 fp32 into 20011 rows: 49 (18), of which the
+// sort takes 16, the join and two launches 6.
 #include <algorithm>
 #include <cmath>
 
@@ -122,13 +126,34 @@ constexpr int kMaxDigit = 10;          // bits of an id taken in one pass
 constexpr int kSortCtas = 8;           // of the cluster
 constexpr int64_t kSortOne = 4096;     // up to so many tokens one block does it: 2 us less than a cluster's barriers
 
+// Rows of a table that are cleared: [first, end).
+struct ClearParams {
+  uint8_t* table;
+  int64_t stride, bytes;  // of a row
+  int64_t first, end;
+};
+
 struct SortParams {
+  ClearParams clear;
   const void* ids;
   uint64_t *a, *b;   // pass 0 writes a, pass 1 writes b, ...
   uint32_t* joins;   // counter that the sums start from zero
   int64_t n, vocab, padding;
   int32_t ids_i64, passes, width;  // passes of `width` bits
+  int32_t ctas;                    // of the sort: the first ones
 };
+
+// Zeros to a row (of elements of 2 or 4 bytes), by `lanes` threads (8 or more) of which this is the `at`-th: single
+// units of two bytes up to a 16-byte boundary, whole vectors, the rest.
+__device__ __forceinline__ void clear_row(uint8_t* row, int64_t bytes, int at, int lanes) {
+  const int head = int(min(bytes, int64_t(-reinterpret_cast<uintptr_t>(row) & 15)));
+  const int64_t vecs = (bytes - head) / 16, tail = head + vecs * 16;
+  if (2 * at < head) *reinterpret_cast<uint16_t*>(row + 2 * at) = 0;
+  for (int64_t i = at; i < vecs; i += lanes) *reinterpret_cast<uint4*>(row + head + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  if (tail + 2 * at < bytes) *reinterpret_cast<uint16_t*>(row + tail + 2 * at) = 0;
+}
+// Threads for a row: a warp or a part of it.
+__device__ __forceinline__ int row_lanes(int64_t bytes) { return bytes > 256 ? 32 : bytes > 128 ? 16 : 8; }
 
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
   uint32_t v;
@@ -149,7 +174,8 @@ __device__ __forceinline__ uint32_t same_digit(uint32_t among, uint32_t d, int w
 // Least significant digit first.  Every warp of the cluster owns a stretch of the
 // array: it counts its digits, 32 keys at a time, the counts are summed over warps,
 // CTAs (distributed shared memory) and digits, and the warp places its keys, in
-// order.
+// order.  The GPU's other SMs meanwhile clear rows at the table's end, whether a token
+// names them or not.
 __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(SortParams p) {
   extern __shared__ uint32_t smem[];
   const int radix = 1 << p.width;
@@ -159,7 +185,14 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(SortParams
   __shared__ uint32_t warp_sum_buf[kSortWarps];
   griddep_release();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = int(cluster_ctarank()), ctas = int(gridDim.x);
+  const int rank = int(cluster_ctarank()), ctas = p.ctas;
+  if (int(blockIdx.x) >= ctas) {
+    const int lanes = row_lanes(p.clear.bytes), per_block = kSortThreads / lanes;
+    const int64_t step = int64_t(gridDim.x - ctas) * per_block;
+    for (int64_t r = p.clear.first + int64_t(blockIdx.x - ctas) * per_block + int(threadIdx.x) / lanes; r < p.clear.end; r += step)
+      clear_row(p.clear.table + r * p.clear.stride, p.clear.bytes, int(threadIdx.x) % lanes, lanes);
+    return;
+  }
   const int64_t per = cdiv(cdiv(p.n, int64_t(ctas) * kSortWarps), 32) * 32;
   const int64_t lo = min(p.n, (int64_t(rank) * kSortWarps + warp) * per), hi = min(p.n, lo + per);
   if (rank == 0 && threadIdx.x == 0) *p.joins = 0u;
@@ -268,6 +301,11 @@ constexpr int kAhead = 4;              // rows under way at once
 constexpr int kMostTeams = 8;          // chunks of a block, where the rows are narrow
 constexpr int kZeroBytes = 128 << 10;  // of the table that a block clears, at most
 constexpr int kZeroLeast = 16 << 10;
+// Bytes that are cleared during the sort, where eight blocks sort and where one does.  (More of them slow the
+// sort, which waits for L2: 8192 tokens into 32000 x 2048 bf16 56 us without, 54 with 48 MB, 67 with 96; 16384 into
+// 151936 x 4096 231, 225, 226.)
+constexpr int64_t kEarly = 48 << 20;
+constexpr int64_t kEarlyOne = 16 << 20;
 constexpr int kZeroRows = 4096;        // at most
 
 struct EmbedBwdParams {
@@ -280,6 +318,7 @@ struct EmbedBwdParams {
   int32_t cols, tiles, chunks, zero_rows, team;  // threads of a chunk
   float scale;
   int32_t accumulate;
+  ClearParams clear;
 };
 
 __device__ __forceinline__ uint32_t key_of(uint64_t e) { return uint32_t(e >> 32); }
@@ -311,12 +350,15 @@ __device__ __forceinline__ void write_row(O* to, float scale, int count, const f
 }
 
 // Zeros to the rows [r0, r1) that no token names.
-template <class O>
-__device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, int64_t r0, int64_t r1, uint32_t* named) {
+__device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, int64_t r0, int64_t r1, uint32_t* named, int* range) {
   const int rows = int(r1 - r0), warps = int(blockDim.x >> 5), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < (rows + 31) / 32; i += blockDim.x) named[i] = 0u;
-  const int64_t lo = lower_bound(p.sorted, 0, p.n, uint32_t(r0)), hi = lower_bound(p.sorted, lo, p.n, uint32_t(r1));
+  if (warp < 2) {  // one warp looks for the first token, one for the last
+    const int64_t at = lower_bound(p.sorted, 0, p.n, uint32_t(warp == 0 ? r0 : r1));
+    if (lane == 0) range[warp] = int(at);
+  }
   __syncthreads();
+  const int64_t lo = range[0], hi = range[1];
   if (hi - lo <= int64_t(rows) * 16) {
     for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) {
       const int r = int(key_of(p.sorted[i]) - uint32_t(r0));
@@ -329,19 +371,10 @@ __device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, int64_t r0, 
     }
   }
   __syncthreads();
-  // a warp or a part of it per row: single elements up to a 16-byte boundary, whole vectors, the rest
-  constexpr int kV = 16 / sizeof(O);
-  const O zero = from_f32<O>(0.f);
-  const int lanes = p.cols > 16 * kV ? 32 : p.cols > 8 * kV ? 16 : 8, at = int(threadIdx.x) % lanes;
-  for (int r = int(threadIdx.x) / lanes; r < rows; r += int(blockDim.x) / lanes) {
-    if ((named[r >> 5] >> (r & 31)) & 1u) continue;
-    O* row = static_cast<O*>(p.dweight) + (r0 + r) * p.ws;
-    const int head = min(p.cols, int((kV - (reinterpret_cast<uintptr_t>(row) / sizeof(O)) % kV) % kV));
-    const int vecs = (p.cols - head) / kV, tail = head + vecs * kV;
-    if (at < head) row[at] = zero;
-    for (int i = at; i < vecs; i += lanes) *reinterpret_cast<uint4*>(row + head + i * kV) = make_uint4(0u, 0u, 0u, 0u);
-    if (tail + at < p.cols) row[tail + at] = zero;
-  }
+  const int lanes = row_lanes(p.clear.bytes);
+  for (int r = int(threadIdx.x) / lanes; r < rows; r += int(blockDim.x) / lanes)
+    if (!((named[r >> 5] >> (r & 31)) & 1u))
+      clear_row(p.clear.table + (r0 + r) * p.clear.stride, p.clear.bytes, int(threadIdx.x) % lanes, lanes);
 }
 
 // kAdd: the sums are added to the table's rows, which are loaded with those of the tokens (28 tokens into 118528 x 64
@@ -358,7 +391,7 @@ __global__ void __launch_bounds__(256, kAdd ? 2 : 3) embed_sum_kernel(EmbedBwdPa
   const int64_t sums = cdiv(p.chunks, teams) * p.tiles;
   if (int64_t(blockIdx.x) >= sums) {
     const int64_t r0 = (int64_t(blockIdx.x) - sums) * p.zero_rows;
-    clear_rows<O>(p, r0, min(p.vocab, r0 + p.zero_rows), named);
+    clear_rows(p, r0, min(p.clear.end, r0 + p.zero_rows), named, ranges[0]);
     return;
   }
   const int team = int(threadIdx.x) / p.team, t = int(threadIdx.x) % p.team;
@@ -546,20 +579,20 @@ cudaError_t launch_embed(EmbedParams& q, cudaStream_t st) {
                                                             : launch_embed<T, O, false>(q, st);
 }
 
-cudaError_t launch_sort(const SortParams& s, cudaStream_t st) {
+cudaError_t launch_sort(const SortParams& s, int num_sms, cudaStream_t st) {
   const int radix = 1 << s.width;
   const size_t smem = size_t(kSortWarps + 2) * radix * 4;
   cudaError_t e = cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (kSortWarps + 2) * (1 << kMaxDigit) * 4);
   if (e != cudaSuccess) return e;
-  const unsigned ctas = s.n <= kSortOne ? 1 : kSortCtas;
+  const unsigned ctas = unsigned(s.ctas), clears = s.clear.end > s.clear.first ? (unsigned(num_sms) - ctas) / ctas * ctas : 0u;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(ctas + clears);
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -575,8 +608,9 @@ cudaError_t launch_sum(EmbedBwdParams& q, cudaStream_t st) {
   // blocks of 160 threads or more: narrow rows have several chunks in one
   const int teams = 256 / threads;
   q.team = threads;
-  const int64_t clear = q.accumulate ? 0 : cdiv(q.vocab, q.zero_rows);
+  const int64_t clear = cdiv(q.clear.end, q.zero_rows);
   const unsigned grid = unsigned(cdiv(q.chunks, teams) * q.tiles + clear);
+  if (grid == 0) return cudaSuccess;  // no tokens, and all is cleared
   return q.accumulate ? launch_dependent(embed_sum_kernel<T, O, kVec, true>, grid, teams * threads, st, q)
                       : launch_dependent(embed_sum_kernel<T, O, kVec, false>, grid, teams * threads, st, q);
 }
@@ -666,7 +700,15 @@ int flce_embedding_backward(const flce_embedding_problem* problem, const void* i
   while ((p->vocab >> bits) != 0) ++bits;
   s.passes = int32_t(cdiv(bits, kMaxDigit));
   s.width = int32_t(cdiv(bits, s.passes));
-  FLCE_TRY(logged(FLCE_LAUNCH_OTHER, st, [&] { return launch_sort(s, st); }));
+  s.ctas = p->tokens <= kSortOne ? 1 : kSortCtas;
+  // rows that are cleared while the tokens are sorted, from the end (frequent tokens have small numbers, mostly)
+  ClearParams& early = s.clear;
+  early.table = static_cast<uint8_t*>(dweight);
+  early.bytes = p->cols * int64_t(elem_size(p->weight_dtype));
+  early.stride = p->weight_stride * int64_t(elem_size(p->weight_dtype));
+  early.end = p->accumulate ? 0 : p->vocab;
+  early.first = std::max<int64_t>(0, early.end - (s.ctas == 1 ? kEarlyOne : kEarly) / early.bytes);
+  FLCE_TRY(logged(FLCE_LAUNCH_OTHER, st, [&] { return launch_sort(s, dev.num_sms, st); }));
   EmbedBwdParams q{};
   q.sorted = s.passes % 2 ? s.a : s.b;
   q.dout = dout;
@@ -679,10 +721,12 @@ int flce_embedding_backward(const flce_embedding_problem* problem, const void* i
   q.ws = p->weight_stride;
   q.cols = int32_t(p->cols);
   q.chunks = int32_t(cdiv(p->tokens, kChunk));
-  // eight blocks to an SM clear the table, if that makes enough for each
-  const int64_t row_bytes = p->cols * int64_t(elem_size(p->weight_dtype));
-  const int64_t clear = std::clamp<int64_t>(p->vocab * row_bytes / (int64_t(dev.num_sms) * 8), kZeroLeast, kZeroBytes);
-  q.zero_rows = int32_t(std::clamp<int64_t>(clear / row_bytes, 1, kZeroRows));
+  // three blocks to an SM clear the rest, if that makes enough for each and not too much
+  q.clear = early;
+  q.clear.first = 0;
+  q.clear.end = early.first;
+  const int64_t clear = std::clamp<int64_t>(q.clear.end * early.bytes / (int64_t(dev.num_sms) * 3), kZeroLeast, kZeroBytes);
+  q.zero_rows = int32_t(std::clamp<int64_t>(clear / early.bytes, 1, kZeroRows));
   q.scale = p->scale;
   q.accumulate = p->accumulate;
   FLCE_TRY(logged(FLCE_LAUNCH_OTHER, st, [&] {
