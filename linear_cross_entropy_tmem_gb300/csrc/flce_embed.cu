@@ -16,9 +16,9 @@
 // no token names, so that these are written once.  The third launch joins the parts,
 // in order.  Nothing depends on the order in which blocks run: same bits every time.
 //
-// 16384 x 4096 bf16 over 151936 rows: lookup 63 us (the copy rate gives 59), gradient
-// 225 (203).  8 rows: 1.9.  4099 x 1283 fp32 into 20011 rows: 49 (18), of which the
-// sort takes 16, the join and two launches 6.
+// 16384 x 4096 bf16 over 151936 rows: lookup to fp32 63 us (the copy rate gives 59),
+// gradient 225 (203).  8 rows: 1.9.  20011 x 1283 fp32 into 4099 rows: 47 (18), of which the
+// sort takes 18, the join and two launches 8.
 #include <algorithm>
 #include <cmath>
 
@@ -297,7 +297,6 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(SortParams
 // Sums over the sorted tokens
 // ---------------------------------------------------------------------------
 constexpr int kChunk = 32;             // sorted tokens of a block: a warp's worth of keys
-constexpr int kAhead = 4;              // rows under way at once
 constexpr int kMostTeams = 8;          // chunks of a block, where the rows are narrow
 constexpr int kZeroBytes = 128 << 10;  // of the table that a block clears, at most
 constexpr int kZeroLeast = 16 << 10;
@@ -380,7 +379,7 @@ __device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, int64_t r0, 
 // kAdd: the sums are added to the table's rows, which are loaded with those of the tokens (28 tokens into 118528 x 64
 // bf16: 21.6 us, 16384 into 151936 x 4096 fp32 124; loaded one by one as their sums end, 24 and 136).
 template <class T, class O, bool kVec, bool kAdd>
-__global__ void __launch_bounds__(256, kAdd ? 2 : 3) embed_sum_kernel(EmbedBwdParams p) {
+__global__ void __launch_bounds__(256, kAdd || !kVec ? 2 : 3) embed_sum_kernel(EmbedBwdParams p) {
   __shared__ uint32_t named[kZeroRows / 32];
   __shared__ uint32_t all_keys[kMostTeams][2 * kChunk + 2];
   __shared__ uint32_t all_tokens[kMostTeams][2 * kChunk];
@@ -446,6 +445,8 @@ __global__ void __launch_bounds__(256, kAdd ? 2 : 3) embed_sum_kernel(EmbedBwdPa
   const uint32_t none = uint32_t(p.vocab);  // the key of tokens without a gradient; those behind the last are above it
   const int end = range[1], enters = range[2], leaves = range[3];
   float* part = p.part + int64_t(chunk) * 2 * p.cols;
+  // rows under way at once; single elements take more registers for them (20011 x 1283 fp32: 47 us, with four rows 49)
+  constexpr int kAhead = kVec || kAdd ? 4 : 8;
   float acc[kElems];
 #pragma unroll
   for (int e = 0; e < kElems; ++e) acc[e] = 0.f;
@@ -564,8 +565,8 @@ template <class T, class O, bool kVec>
 cudaError_t launch_embed(EmbedParams& q, cudaStream_t st) {
   const int threads = row_threads(q.cols, kVec);
   q.tiles = int32_t(cdiv(q.cols, int64_t(threads) * kElems));
-  // Two rows at once where that leaves enough blocks for every SM: 16384 x 4096 bf16 63 us (the copy
-  // rate gives 59); one at once 65, four 73, eight 97.
+  // Two rows at once where that leaves enough blocks for every SM: 16384 x 4096 bf16 to fp32 63 us (the
+  // copy rate gives 59); one at once 65, four 73, eight 97.
   if (cdiv(q.tokens, 2) * q.tiles >= 1024) {
     embed_kernel<T, O, kVec, 2><<<unsigned(cdiv(q.tokens, 2) * q.tiles), threads, 0, st>>>(q);
   } else {
