@@ -302,7 +302,7 @@ constexpr int kZeroBytes = 128 << 10;  // of the table that a block clears, at m
 constexpr int kZeroLeast = 16 << 10;
 // Bytes that are cleared during the sort, where eight blocks sort and where one does.  (More of them slow the
 // sort, which waits for L2: 8192 tokens into 32000 x 2048 bf16 56 us without, 54 with 48 MB, 67 with 96; 16384 into
-// 151936 x 4096 231, 225, 226.)
+// 151936 x 4096 230, 225, 225.)
 constexpr int64_t kEarly = 48 << 20;
 constexpr int64_t kEarlyOne = 16 << 20;
 constexpr int kZeroRows = 4096;        // at most

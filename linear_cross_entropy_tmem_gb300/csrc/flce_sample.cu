@@ -22,7 +22,7 @@
 // finishes them.  Else the entries of those bins are listed, or, where
 // they are many (ties), found by histograms over ever smaller intervals of (value,
 // index).  The mass that top-p is of takes a pass that forms every weight, which is
-// what bounds the largest calls: 256 x 262144 fp32 with top-p takes 341 us, of which
+// what bounds the largest calls: 256 x 262144 fp32 with top-p takes 324 to 341 us, of which
 // reading is 60 and the weights 150; about 100 instructions per entry fill 60 % of
 // the issue slots.
 #include <algorithm>
