@@ -43,7 +43,7 @@ constexpr int kMaxCtas = 16;           // of a cluster
 constexpr int kBins = 2048;
 constexpr float kBinsPerOctave = 64.f; // of the first histogram: 32 octaves below the largest weight
 constexpr uint32_t kList = kThreadsS;  // entries that one block finishes, one per thread
-constexpr int64_t kMaxVocab = 1 << 20; // a CTA's limb sums (65536 entries of 16 bits) fit 32 bits
+constexpr int64_t kMaxVocab = 1 << 20; // weights are in units of 2^-42 of the largest there
 
 __host__ __device__ constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -67,7 +67,7 @@ struct Pair {
 };
 
 struct Shared {
-  uint32_t hist[4][kBins];   // entries, and three limbs of 16 bits of their weights
+  uint32_t hist[3][kBins];   // entries, and the low and the high 32 bits of their weights' sums
   uint32_t first[kBins];     // the first histogram, of the whole row: entries up to each bin's end
   uint64_t table[32];        // 2^(62 - j / 32)
   uint2 pairs[32];           // 2^(31 - j / 32) as an integer and as a float
@@ -396,11 +396,14 @@ struct Cluster {
   }
 };
 
+// A bin can hold a whole row (equal logits), whose mass is below 2^62.  The addition that takes the low word past 2^32
+// sees it, and carries: no number of entries is too many.  (One 64-bit atomic would be a loop of compare-and-swap.)
 __device__ __forceinline__ void add_entry(Shared& s, int bin, uint64_t w) {
+  const uint32_t lo = uint32_t(w);
   atomicAdd(&s.hist[0][bin], 1u);
-  atomicAdd(&s.hist[1][bin], uint32_t(w) & 0xffffu);
-  atomicAdd(&s.hist[2][bin], uint32_t(w >> 16) & 0xffffu);
-  atomicAdd(&s.hist[3][bin], uint32_t(w >> 32));
+  const uint32_t sum = atomicAdd(&s.hist[1][bin], lo) + lo;
+  const uint32_t hi = uint32_t(w >> 32) + (sum < lo);
+  if (hi) atomicAdd(&s.hist[2][bin], hi);
 }
 __device__ __forceinline__ void clear_hist(Shared& s, int parts) {
   __syncthreads();
@@ -438,8 +441,7 @@ __device__ __forceinline__ void descend(Shared& s, Cluster& cl, Interval& v, int
         const uint32_t at = map_to_cta(smem_u32(&s.hist[0][bin0 + k]), uint32_t(c));
         n[k] += ld_cluster(at);
         if (kMass)
-          m[k] += ld_cluster(at + kBins * 4) + (uint64_t(ld_cluster(at + kBins * 8)) << 16) +
-                  (uint64_t(ld_cluster(at + kBins * 12)) << 32);
+          m[k] += ld_cluster(at + kBins * 4) + (uint64_t(ld_cluster(at + kBins * 8)) << 32);
       }
     }
     a += n[k];
@@ -494,7 +496,7 @@ __device__ __forceinline__ void narrow(Shared& s, Cluster& cl, const Slice<T>& s
                                        uint64_t target) {
   constexpr int kV = Slice<T>::kV;
   while (v.n > 1) {
-    clear_hist(s, kMass ? 4 : 1);
+    clear_hist(s, kMass ? 3 : 1);
     const int shift = shift_of(v);
     // values outside [lowest, highest] are outside the interval (its end is not of it)
     const float highest = value_of(uint32_t(v.lo >> 32)), lowest = value_of(uint32_t((v.hi - 1) >> 32));
@@ -560,8 +562,8 @@ __device__ __forceinline__ uint32_t bin_edge(int b, float top, float per_unit) {
 template <bool kMass>
 __device__ __forceinline__ uint64_t block_select(Shared& s, uint64_t x, bool in, uint64_t w, uint64_t lo, uint64_t hi,
                                                  uint64_t base, uint64_t target) {
-  uint32_t* const number = s.hist[2];
-  unsigned long long* const mass = reinterpret_cast<unsigned long long*>(s.hist[3]);
+  uint32_t* const number = s.hist[1];
+  unsigned long long* const mass = reinterpret_cast<unsigned long long*>(s.hist[2]);
   const uint32_t t = threadIdx.x;
   while (true) {
     const int shift = max(0, 64 - __clzll((hi - lo - 1) | 1) - 10);  // to kList bins
@@ -1016,7 +1018,7 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
         // The mass of the whole, of what stands before these bins, and a list of their entries (with `few`, of
         // those before them too), or their histogram where they are many.
         const bool listing = round == 0 && (few || through - before_lo <= kList);
-        if (!listing) clear_hist(s, 4);
+        if (!listing) clear_hist(s, 3);
         const int shift = shift_of(v);
         // (whole keys) larger logits than z_hi stand before the bins, up to z_lo behind them
         z_hi = value_of(uint32_t(v.lo >> 32));
@@ -1120,7 +1122,7 @@ __global__ void __launch_bounds__(kThreadsS, 1) sample_kernel(SampleParams p) {
             cut_behind(v.hi - 1);
           }
         }
-        // else the estimate was too far off: every place
+        // else the estimate was too far off: every place (where the sums, which are exact, reach the target)
         v.lo = uint64_t(key_of(top)) << 32;
         v.hi = uint64_t(key_of(-INFINITY)) << 32;
       }
