@@ -366,8 +366,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int seq = 0;
     for (int u = first; u < units; u += stride, ++seq) {
       if ((seq & 1) != grp) continue;
-      bool ok = stage_wait(&sm.tfull[grp], phase, sm.ctl, status);
-      if constexpr (kTurned) ok = group_all(grp, ok);  // (they give up as one)
+      // (the warp gives up as one, and where the group's warps share a buffer, they do)
+      bool ok;
+      if constexpr (kTurned) {
+        ok = group_all(grp, stage_wait(&sm.tfull[grp], phase, sm.ctl, status));
+      } else {
+        ok = warp_wait(&sm.tfull[grp], phase, sm.ctl, status);
+      }
       if (!ok) break;
       tc_fence_after();
       int m, n;
