@@ -28,6 +28,7 @@
 // quantisation (the launch before this one) is waited for.  Waits are bounded as
 // in the other products.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cuda.h>
 
@@ -575,7 +576,8 @@ int flce_mxfp4_logits(const flce_mxfp4_logits_problem* problem, const void* hidd
   q.bias_dtype = p->bias_dtype;
   q.scale = p->logit_scale;
   q.cap = p->softcap;
-  q.inv_cap = p->softcap > 0.f ? 1.f / p->softcap : 0.f;
+  // (1 / cap of the smallest numbers is beyond fp32: an infinity would make a logit of 0 not a number)
+  q.inv_cap = p->softcap > 0.f ? std::min(1.f / p->softcap, FLT_MAX) : 0.f;
   int* status = reinterpret_cast<int*>(ws);
   return logged(FLCE_LAUNCH_OTHER, st, [&] {
     if (p->out_dtype == FLCE_F32) return launch_logits<float>(a, b, q, status, dev.num_sms, st);
