@@ -46,7 +46,12 @@ def _want(dtype, what):
 
 
 def _pad(padding_idx):
-    return -1 if padding_idx is None else int(padding_idx)
+    if padding_idx is None:
+        return -1
+    if padding_idx < 0:  # (torch's embedding counts it from the table's end; here -1 is what tokens without an id have)
+        raise ValueError(f"flce: padding_idx must be None or an id of the table, got {padding_idx}: negative numbers are "
+                         "not counted from its end")
+    return int(padding_idx)
 
 
 def flce_embedding(weight: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0,
@@ -77,7 +82,8 @@ def flce_embedding_backward(dout: torch.Tensor, ids: torch.Tensor, vocab: int, *
                             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient [vocab, D] of the table, from that of the rows (see ``flce_embedding_backward``), in ``dtype`` (dout's).
     With ``dweight``, a matrix such as the gradient that a tied head's backward left, the rows' sums are added to it
-    in place (rows without a token are left as they are), and it is returned."""
+    in place (rows without a token are left as they are), and it is returned.  ``padding_idx``: as in
+    :func:`embedding`."""
     res = _call("embedding_backward", dout, ids, vocab, scale, _pad(padding_idx), _want(dtype, "dweight"), dweight,
                 workspace)
     if res is not None:
@@ -120,6 +126,7 @@ class Embedding(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, weight, ids, scale, padding_idx, out_dtype):
+        _pad(padding_idx)
         ctx.save_for_backward(ids)
         ctx.vocab, ctx.dtype, ctx.scale, ctx.padding = weight.shape[0], weight.dtype, scale, padding_idx
         return flce_embedding(weight, ids, scale=scale, out_dtype=out_dtype)
@@ -137,7 +144,7 @@ class Embedding(torch.autograd.Function):
 def embedding(weight: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, padding_idx: Optional[int] = None,
               out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """``weight[ids] * scale`` with the table's gradient: rows of ids outside [0, V) are zeros, and neither they nor
-    ``padding_idx`` have one.
+    ``padding_idx`` have one (an id of the table; a negative number is refused, it does not count from the end).
 
     A backward captured into a CUDA graph: while an earlier graph of the same leaf lives, autograd adds to the leaf on
     the stream on which that graph was recorded.  Record it on the capturing stream, or drop it before the capture."""
