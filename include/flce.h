@@ -681,8 +681,12 @@ typedef struct {
  *   token[b]   = the first that stays, in index order, up to which the weight of
  *                those that stay is more than uniform[b] of their whole
  *   logprob[b] = log of its part of that whole;  kept[b] = how many stay
- * Weights have errors below 2^-31 of themselves and are summed exactly: the same
- * bits from call to call, and equal logits have equal weights.
+ * Weights are whole units of 2^-b of the largest, b = 46 or 62 - ceil(log2 V) if
+ * that is less.  Their errors are below 2^-35 of themselves where they are at least
+ * 2^-6 of the largest, below 2^-27 elsewhere, and a unit.  Those below half a unit
+ * are 0 (never chosen, and dropped by any min_p > 0).
+ * They are summed exactly: the same bits from call to call and from batch to
+ * batch, and equal logits have equal weights.
  *   logits   [B, V]
  *   uniform  [B] fp32 in [0, 1) (below: 0, and NaN; above: just below 1)
  *   temperature  [B] fp32 or NULL (1).  0, below, or NaN: greedy, the lowest index of

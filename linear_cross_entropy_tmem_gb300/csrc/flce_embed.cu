@@ -16,9 +16,10 @@
 // no token names, so that these are written once.  The third launch joins the parts,
 // in order.  Nothing depends on the order in which blocks run: same bits every time.
 //
-// 16384 x 4096 bf16 over 151936 rows: lookup to fp32 63 us (the copy rate gives 59),
-// gradient 225 (203).  8 rows: 1.9.  20011 x 1283 fp32 into 4099 rows: 47 (18), of which the
-// sort takes 18, the join and two launches 8.
+// 16384 x 4096 bf16 over 151936 rows, one token in 16 without an id: lookup to fp32 63 us (the
+// copy rate gives 58 for the rows of all tokens, 54 for those of 12244 different ones), gradient
+// 227 (202).  8 rows: 2.  20011 x 1283 fp32 into 4099 rows: 46 (17), of which the sort takes 18,
+// the join and two launches 8.  The sort has eight SMs, whatever the number of tokens.
 #include <algorithm>
 #include <cmath>
 
@@ -566,7 +567,7 @@ cudaError_t launch_embed(EmbedParams& q, cudaStream_t st) {
   const int threads = row_threads(q.cols, kVec);
   q.tiles = int32_t(cdiv(q.cols, int64_t(threads) * kElems));
   // Two rows at once where that leaves enough blocks for every SM: 16384 x 4096 bf16 to fp32 63 us (the
-  // copy rate gives 59); one at once 65, four 73, eight 97.
+  // copy rate gives 58); one at once 65, four 73, eight 97.
   if (cdiv(q.tokens, 2) * q.tiles >= 1024) {
     embed_kernel<T, O, kVec, 2><<<unsigned(cdiv(q.tokens, 2) * q.tiles), threads, 0, st>>>(q);
   } else {

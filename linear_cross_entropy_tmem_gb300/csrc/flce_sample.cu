@@ -11,10 +11,11 @@
 // the row stay on chip, or nearly.
 //
 // Whole numbers come out of sums here (which entries are kept, which is chosen),
-// so weights are integers: w_i in units of 2^-bits of the largest, from a table and a
-// polynomial with an error below 2^-31 of w_i (2^-37 where w_i is at least 2^-6 of
-// the largest: those carry the error of the sums).  Integer sums do not depend on
-// their order, and equal logits have equal weights.
+// so weights are integers: w_i in units of 2^-bits of the largest (bits is 46, or as
+// many as leave the sum of all below 2^62), from a table and a polynomial with an
+// error below 2^-27 of w_i and a unit (found: 2^-28.6), or 2^-35 (2^-36) where w_i is at
+// least 2^-6 of the largest: those carry the error of the sums, mostly.  Integer sums do
+// not depend on their order, and equal logits have equal weights.
 //
 // Top-k and top-p cut the ranking at one place.  A first histogram, over the distance
 // from the maximum in steps of 2^(1/64) of the weight, names the bins in which
@@ -22,9 +23,12 @@
 // finishes them.  Else the entries of those bins are listed, or, where
 // they are many (ties), found by histograms over ever smaller intervals of (value,
 // index).  The mass that top-p is of takes a pass that forms every weight, which is
-// what bounds the largest calls: 256 x 262144 fp32 with top-p takes 324 to 341 us, of which
-// reading is 60 and the weights 150; about 100 instructions per entry fill 60 % of
-// the issue slots.
+// what takes longest in the largest calls: 256 x 262144 fp32 with top-p takes 324 to 337 us,
+// of which the first read is 60 and the weights 150.  About 100 instructions per entry fill
+// 60 % of the issue slots.  The others are idle: where a row has one CTA, 82 % of it is read
+// again in every later pass, one vector per lane at a time (how much of the time that is
+// was not measured).  Rows of few different values are slow: their entries add to the same bins
+// (256 rows of 262144, all but one equal, 2.9 ms).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -224,7 +228,9 @@ struct Weigh {
   // Weights of two entries, 0 where np is not above `end`.  -np = n / 32 + r exactly; 2^-y = 2^(-n / 32) 2^x
   // with x = -(r + e), at most 1 / 64 in size: a table's value, a shift, and a Taylor polynomial
   // whose fourth power leaves 2^-39.  The last bit that stays is set, which makes up for those cut
-  // off.  (Above kNear, weights over 2^-6 of the largest, `precise` takes their place.)
+  // off.  In units of the table's last bit, 2^-30 of w at most: the table is cut by 1; x, q and its
+  // product are rounded by 0.7, 1 and 1.5; the last bit adds 1: below 2^-27.  (Above kNear, weights
+  // over 2^-6 of the largest, `precise` takes their place.)
   __device__ __forceinline__ void pair(float z0, float z1, Term (&t)[2], float (&np)[2]) const {
     uint64_t p2, e;
     distance(f2_pack(z0, z1), p2, e);

@@ -224,7 +224,8 @@ def mxfp4_logits(hidden: torch.Tensor, weight: MxFp4, bias: Optional[torch.Tenso
     """Logits [..., V] of hidden states [..., D] from a head's weight in 4 bits (see ``flce_mxfp4_logits``): the hidden
     states are quantised in the call, the product runs on both in 4 bits.  ``out_dtype`` is hidden's dtype, or any of
     the three; ``out`` a matrix of rows to write.  Nothing is recorded for autograd; a given ``out`` counts as changed
-    in place."""
+    in place.  The kernel's waits are bounded: to see whether it gave one up, give a ``workspace`` (of uint8) and read its
+    status with :func:`flce_read_device_status`; without one the status is dropped with the call's own workspace."""
     res = _call("mxfp4_logits", hidden, weight.codes, weight.scales, weight.cols, bias, logit_scale, softcap,
                 _want(out_dtype, "out"), out, workspace)
     if res is not None:
