@@ -25,7 +25,7 @@
 // index).  The mass that top-p is of takes a pass that forms every weight, which is
 // what takes longest in the largest calls: 256 x 262144 fp32 with top-p takes 324 to 337 us,
 // of which the first read is 60 and the weights 150.  About 100 instructions per entry fill
-// 60 % of the issue slots.  The others are idle: where a row has one CTA, 82 % of it is read
+// 60 % of the issue slots.  The others are idle: where a row has one CTA, 81 % of it is read
 // again in every later pass, one vector per lane at a time (how much of the time that is
 // was not measured).  Rows of few different values are slow: their entries add to the same bins
 // (256 rows of 262144, all but one equal, 2.9 ms).
